@@ -16,6 +16,9 @@
  *    per-row upstream gradient, from the forward's row loss.
  *  - gh_chunked_linear_loss: `chunked_linear_loss` — the chunk loop of
  *    gh_linear_ce with a caller-provided loss and logits gradient per chunk.
+ *  - gh_token_logprobs, gh_token_logprobs_vjp, gh_topk_distill: log-probabilities
+ *    with entropy and alternatives, their gradient, and distillation from a
+ *    teacher's top logits; the Greyhound API has no counterpart.
  *  - gh_linear_ce: `chunked_linear_cross_entropy` — logits = inputs @ weight.T
  *    computed one row chunk at a time and never materialised in full; per
  *    chunk the logits gradient G gives grad_inputs[chunk] = G @ weight and
@@ -36,8 +39,9 @@
  *
  * Common rules for every entry point:
  *  - Tensor pointers are DEVICE pointers owned by the caller, row-major and
- *    contiguous (row stride = number of columns).  The library keeps no
- *    pointer after the call returns.
+ *    contiguous (row stride = number of columns; where an entry point takes
+ *    `ld`, that many elements).  The library keeps no pointer after the call
+ *    returns.
  *  - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *    stream).  Work is enqueued on it and the call returns without waiting;
  *    outputs are valid once the stream reaches that point.  The library
@@ -268,6 +272,107 @@ gh_status_t gh_selective_log_softmax(const void* logits, const int64_t* index, i
                                      gh_dtype_t dtype, float* out, void* stream);
 
 /*
+ * gh_token_logprobs — the log-probability of one given token per row, the
+ * row's entropy and its most probable alternatives, from one pass over the
+ * logits (serving's `logprobs`, scoring, policy gradients, writing out a
+ * teacher's top logits).  With z = x / temperature and
+ * lse = log sum_j exp(z_j), log p_j = z_j - lse:
+ *     logprob = log p_t        entropy = -sum_j p_j log p_j   (0 log 0 = 0)
+ *     top_index[k], top_logprob[k]: the k-th logit by (value descending, index
+ *     ascending) and its log-probability, k < top_k
+ *
+ *   logits   [B, V] of `dtype` (GH_F32 or GH_BF16), device; rows `ld` elements
+ *            apart (ld >= V), so a head padded to a round size is read in place.
+ *   index    [B] int64, device: the given tokens.
+ *   B >= 0, V >= 1 (V < 2^31).
+ *   ignore_index  rows with this index are not read: logprob, entropy and lse
+ *            are 0, the alternatives -inf with index -1.
+ *   temperature   in [1e-4, 1e4].
+ *   top_k    0 <= top_k <= V, at most GH_MAX_TOP_K.
+ *   logprob, entropy, lse  [B] float32, device, written.
+ *   top_logprob  [B, top_k] float32, top_index [B, top_k] int64, device,
+ *            written (not used for top_k = 0).  Logits of -inf take part, last.
+ * A row without a distribution (a NaN or +inf logit, or -inf logits only) gets
+ * NaN values and alternatives with index -1.  An index outside [0, V) that is
+ * not ignore_index: the same, and GH_ERR_TARGET_RANGE is recorded.
+ * GH_ERR_UNSUPPORTED for top_k > GH_MAX_TOP_K.
+ */
+#define GH_MAX_TOP_K 128
+gh_status_t gh_token_logprobs(const void* logits, int64_t ld, const int64_t* index, int64_t B, int64_t V,
+                              gh_dtype_t dtype, int64_t ignore_index, float temperature, int64_t top_k,
+                              float* logprob, float* entropy, float* lse, float* top_logprob, int64_t* top_index,
+                              void* stream);
+
+/*
+ * gh_token_logprobs_vjp — the logits gradient of gh_token_logprobs' logprob
+ * and entropy for an upstream gradient of each per row (g_l, g_H), in one
+ * sweep from the forward's lse and entropy:
+ *     grad_j = (1 / temperature) (g_l [j == t] - p_j (g_l + g_H (log p_j + entropy)))
+ *
+ *   logits, ld, index, B, V, dtype, ignore_index, temperature  as given to
+ *            gh_token_logprobs.
+ *   lse, entropy  [B] float32, device: what it returned (values of ignored
+ *            rows are not read).
+ *   g_logprob [B] float32, device.
+ *   g_entropy [B] float32, device, or NULL for none.
+ *   grad     [B, V] of `dtype`, rows ld_grad apart, device, written (round to
+ *            nearest even; the columns from V to ld_grad are left as they
+ *            are).  grad == logits with ld_grad == ld is allowed (in place);
+ *            any other overlap is not.
+ * Rows whose index equals ignore_index get a zero gradient row; an index
+ * outside [0, V) likewise, and records GH_ERR_TARGET_RANGE.  No scratch.
+ */
+gh_status_t gh_token_logprobs_vjp(const void* logits, int64_t ld, const int64_t* index, int64_t B, int64_t V,
+                                  gh_dtype_t dtype, int64_t ignore_index, float temperature, const float* lse,
+                                  const float* entropy, const float* g_logprob, const float* g_entropy, void* grad,
+                                  int64_t ld_grad, void* stream);
+
+/*
+ * gh_topk_distill — distillation from a teacher's top logits: the loss and
+ * the student's logits gradient in one call.  A row has K stored entries
+ * (id, value), as gh_token_logprobs writes them; an entry whose id is -1 or
+ * whose value is -inf is none.  With T = temperature, p = softmax(x / T), q the
+ * teacher's probabilities of the row's entries and Q = sum_k q_k:
+ *     row loss = T^2 sum_k q_k (log q_k - log p_{id_k})       (0 log 0 = 0)
+ *     grad_j   = scale T (Q p_j - sum_{k: id_k = j} q_k)
+ *     scale    = 1 / max(n, 1) for GH_REDUCTION_MEAN, 1 for SUM
+ *     loss     = scale * sum of row losses
+ * where n counts the rows with an entry.  Rows without one have no loss and a
+ * zero gradient, and their logits are not read.
+ *
+ *   logits   [B, V] of `dtype`, device, rows `ld` elements apart (ld >= V).
+ *   teacher_index  [B, K] int64, teacher_logits [B, K] float32, device; an id
+ *            may come more than once (its entries add up).
+ *   1 <= K <= GH_MAX_TOP_K (GH_ERR_UNSUPPORTED above).
+ *   temperature   in [1e-4, 1e4].
+ *   renormalize   1: q = softmax over the row's entries of value / T (values
+ *            are logits, or log-probabilities at temperature 1);
+ *            0: q = exp(value) (log-probabilities at temperature T, their sum
+ *            at most 1).
+ *   n_valid_total  device int64 scalar in place of n (a batch in chunks or
+ *            shards: the sum of their gh_distill_count), or NULL to count.
+ *   loss     device float32 scalar, written.
+ *   row_loss optional device float32 [B] (NULL: not returned), written with
+ *            the row losses before reduction.
+ *   grad     [B, V] of `dtype`, rows ld_grad apart, device, written (columns
+ *            from V on are left), or NULL for the loss alone (evaluation).
+ *            grad == logits with ld_grad == ld is allowed; no other overlap.
+ * A row without a distribution (see gh_token_logprobs) or with a NaN value
+ * gives a NaN loss and gradient row.  An id outside [0, V) other than -1 is
+ * treated as none and records GH_ERR_TARGET_RANGE.
+ *
+ * gh_distill_count — count = number of rows with an entry (int64 device
+ * scalar, written).
+ */
+gh_status_t gh_topk_distill(const void* logits, int64_t ld, const int64_t* teacher_index,
+                            const float* teacher_logits, int64_t B, int64_t V, int64_t K, gh_dtype_t dtype,
+                            float temperature, int renormalize, gh_reduction_t reduction,
+                            const int64_t* n_valid_total, float* loss, float* row_loss, void* grad, int64_t ld_grad,
+                            void* stream);
+gh_status_t gh_distill_count(const int64_t* teacher_index, const float* teacher_logits, int64_t B, int64_t K,
+                             int64_t V, int64_t* count, void* stream);
+
+/*
  * gh_linear_ce — chunked fused linear cross-entropy (Greyhound
  * `chunked_linear_cross_entropy` over `chunked_linear_loss`).
  *
@@ -343,7 +448,10 @@ typedef enum {
   GH_KERNEL_DX_GEMM = 3,       /* linear-CE: grad_inputs[chunk] = G_c @ W */
   GH_KERNEL_DW_GEMM = 4,       /* linear-CE: grad_weight (+)= G_c^T @ X_c */
   GH_KERNEL_CE_VJP = 5,        /* gh_ce_vjp */
-  GH_KERNEL_KINDS = 6
+  GH_KERNEL_LOGPROBS = 6,      /* gh_token_logprobs */
+  GH_KERNEL_LOGPROBS_VJP = 7,  /* gh_token_logprobs_vjp */
+  GH_KERNEL_DISTILL = 8,       /* gh_topk_distill */
+  GH_KERNEL_KINDS = 9
 } gh_kernel_t;
 
 /* gh_profile_enable(1) discards earlier records and starts recording a pair

@@ -8,6 +8,9 @@ exception is raised.
 
 * ``gh_ce_fwd_bwd`` — Greyhound ``cross_entropy``: loss and logits gradient of
   materialised ``[B, V]`` logits in one call.
+* ``gh_token_logprobs`` / ``gh_token_logprobs_vjp`` — log-probabilities of given
+  tokens with the rows' entropy and most probable alternatives, and their gradient.
+* ``gh_topk_distill`` — distillation from a teacher's top logits.
 * ``gh_linear_ce`` — Greyhound ``chunked_linear_cross_entropy``: loss,
   ``grad_inputs`` and ``grad_weight`` of ``inputs @ weight.T`` computed chunk
   by chunk, without the full logits.
@@ -34,6 +37,7 @@ GH_ERR_TARGET_RANGE = 6
 GH_REDUCTION = {"mean": 0, "sum": 1}
 GH_ACCUM = {"fp32": 0, "weight": 1}
 GH_F32, GH_BF16 = 0, 1
+GH_MAX_TOP_K = 128
 
 
 class GhError(RuntimeError):
@@ -95,6 +99,17 @@ def lib() -> ctypes.CDLL:
     L.gh_ce_vjp.restype = c_int
     L.gh_selective_log_softmax.argtypes = [c_void_p, c_void_p, c_int64, c_int64, c_int, c_void_p, c_void_p]
     L.gh_selective_log_softmax.restype = c_int
+    L.gh_token_logprobs.argtypes = [c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int, c_int64, c_float, c_int64,
+                                    c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]
+    L.gh_token_logprobs.restype = c_int
+    L.gh_token_logprobs_vjp.argtypes = [c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int, c_int64, c_float,
+                                        c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p]
+    L.gh_token_logprobs_vjp.restype = c_int
+    L.gh_topk_distill.argtypes = [c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_int64, c_int64, c_int, c_float,
+                                  c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p]
+    L.gh_topk_distill.restype = c_int
+    L.gh_distill_count.argtypes = [c_void_p, c_void_p, c_int64, c_int64, c_int64, c_void_p, c_void_p]
+    L.gh_distill_count.restype = c_int
     L.gh_linear_ce.argtypes = [c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int64, c_int64, c_int,
                                c_int64, c_int, c_float, c_void_p, c_void_p, c_void_p, c_void_p]
     L.gh_linear_ce.restype = c_int
@@ -514,6 +529,198 @@ def gh_selective_log_softmax(logits, index, *, out=None, stream=None):
     return out
 
 
+def _rows(logits):
+    """(B, V, row stride, dtype code) of [B, V] logits whose rows are dense."""
+    import torch
+    _need(logits.dim() == 2 and logits.is_cuda, "logits: CUDA [B, V]")
+    _need(logits.dtype in (torch.float32, torch.bfloat16), "logits dtype must be float32 or bfloat16")
+    B, V = logits.shape
+    ld, col = logits.stride()
+    _need(V >= 1 and (col == 1 or V == 1), "logits: the last dimension must be dense")
+    if B <= 1:
+        ld = V
+    _need(ld >= V, "logits: rows must not overlap")
+    return B, V, ld, GH_F32 if logits.dtype == torch.float32 else GH_BF16
+
+
+def _row_tensor(t, name: str, dtype, shape, device) -> None:
+    if not (t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+        raise ValueError(f"{name}: contiguous {dtype} {list(shape)} on {device}")
+
+
+def _grad_like(grad, logits, B, V, ld):
+    """The gradient's tensor and row stride (by default laid out as the logits)."""
+    import torch
+    if grad is None:
+        return torch.empty_strided((B, V), (ld, 1), dtype=logits.dtype, device=logits.device), ld
+    if grad is logits:
+        return grad, ld
+    _need(grad.shape == logits.shape and grad.dtype == logits.dtype and grad.device == logits.device, "grad mismatch")
+    ldg, col = grad.stride()
+    if B <= 1:
+        ldg = V
+    _need((col == 1 or V == 1) and ldg >= V, "grad: dense rows that do not overlap")
+    return grad, ldg
+
+
+def _on_device_of(fn):
+    """Run `fn` with its first argument's device current (the library launches on
+    the current device, and the default stream is that device's)."""
+    import functools
+
+    @functools.wraps(fn)
+    def call(first, *args, **kwargs):
+        import torch
+        if first.is_cuda and first.device.index != torch.cuda.current_device():
+            with torch.cuda.device(first.device):
+                return fn(first, *args, **kwargs)
+        return fn(first, *args, **kwargs)
+    return call
+
+
+@_on_device_of
+def gh_token_logprobs(logits, index, top_k: int = 0, temperature: float = 1.0, ignore_index: int = -100, *,
+                      logprob=None, entropy=None, lse=None, top_logprob=None, top_index=None, stream=None):
+    """Log-probability of one given token per row, the row's entropy and its
+    ``top_k`` most probable alternatives (one call into ``gh_token_logprobs``).
+
+    ``logits`` CUDA [B, V] float32 or bfloat16 with dense rows (any row stride
+    >= V), ``index`` CUDA int64 [B]; ``top_k`` at most 128 and V.  Everything is
+    of ``logits / temperature`` (in [1e-4, 1e4]).  Returns ``(logprob, entropy,
+    lse, top_logprob, top_index)``: float32 [B] three times, float32 and int64
+    [B, top_k] (None for ``top_k=0``).  Rows whose index is ``ignore_index``
+    give 0, 0, 0, -inf and -1.  Outputs are allocated when not given.
+    """
+    import torch
+    B, V, ld, dtype = _rows(logits)
+    dev = logits.device
+    _row_tensor(index, "index", torch.int64, (B,), dev)
+    top_k = int(top_k)
+    _need(0 <= top_k <= V, "top_k must be between 0 and V")
+    f32 = torch.float32
+    if logprob is None:
+        logprob = torch.empty(B, dtype=f32, device=dev)
+    else:
+        _row_tensor(logprob, "logprob", f32, (B,), dev)
+    if entropy is None:
+        entropy = torch.empty(B, dtype=f32, device=dev)
+    else:
+        _row_tensor(entropy, "entropy", f32, (B,), dev)
+    if lse is None:
+        lse = torch.empty(B, dtype=f32, device=dev)
+    else:
+        _row_tensor(lse, "lse", f32, (B,), dev)
+    if top_k:
+        if top_logprob is None:
+            top_logprob = torch.empty((B, top_k), dtype=f32, device=dev)
+        else:
+            _row_tensor(top_logprob, "top_logprob", f32, (B, top_k), dev)
+        if top_index is None:
+            top_index = torch.empty((B, top_k), dtype=torch.int64, device=dev)
+        else:
+            _row_tensor(top_index, "top_index", torch.int64, (B, top_k), dev)
+    else:
+        top_logprob = top_index = None
+    st = lib().gh_token_logprobs(_ptr(logits), ld, _ptr(index), B, V, dtype, int(ignore_index), float(temperature),
+                                 top_k, _ptr(logprob), _ptr(entropy), _ptr(lse), _ptr(top_logprob), _ptr(top_index),
+                                 _stream_handle(stream))
+    _check(st, "gh_token_logprobs")
+    return logprob, entropy, lse, top_logprob, top_index
+
+
+@_on_device_of
+def gh_token_logprobs_vjp(logits, index, lse, entropy, g_logprob, g_entropy=None, temperature: float = 1.0,
+                          ignore_index: int = -100, *, grad=None, stream=None):
+    """Logits gradient of ``gh_token_logprobs``' log-probability and entropy (one
+    call into ``gh_token_logprobs_vjp``).
+
+    ``logits``, ``index``, ``temperature`` and ``ignore_index`` as given to
+    ``gh_token_logprobs``, ``lse`` and ``entropy`` as it returned; ``g_logprob``
+    and ``g_entropy`` (None for none) the upstream gradients, float32 [B].
+    ``grad`` (optional output, may be ``logits`` itself) is allocated with the
+    logits' row stride when not given.  Returns ``grad``.
+    """
+    import torch
+    B, V, ld, dtype = _rows(logits)
+    dev = logits.device
+    _row_tensor(index, "index", torch.int64, (B,), dev)
+    _row_tensor(lse, "lse", torch.float32, (B,), dev)
+    _row_tensor(entropy, "entropy", torch.float32, (B,), dev)
+    _row_tensor(g_logprob, "g_logprob", torch.float32, (B,), dev)
+    if g_entropy is not None:
+        _row_tensor(g_entropy, "g_entropy", torch.float32, (B,), dev)
+    grad, ldg = _grad_like(grad, logits, B, V, ld)
+    st = lib().gh_token_logprobs_vjp(_ptr(logits), ld, _ptr(index), B, V, dtype, int(ignore_index),
+                                     float(temperature), _ptr(lse), _ptr(entropy), _ptr(g_logprob), _ptr(g_entropy),
+                                     _ptr(grad), ldg, _stream_handle(stream))
+    _check(st, "gh_token_logprobs_vjp")
+    return grad
+
+
+@_on_device_of
+def gh_distill_count(teacher_index, teacher_logits, V: int, *, count=None, stream=None):
+    """Number of rows with a teacher entry (CUDA int64 scalar tensor): what
+    ``gh_topk_distill`` divides a mean by."""
+    import torch
+    _need(teacher_index.dim() == 2 and teacher_index.is_cuda, "teacher_index: CUDA [B, K]")
+    B, K = teacher_index.shape
+    dev = teacher_index.device
+    _row_tensor(teacher_index, "teacher_index", torch.int64, (B, K), dev)
+    _row_tensor(teacher_logits, "teacher_logits", torch.float32, (B, K), dev)
+    if count is None:
+        count = torch.empty((), dtype=torch.int64, device=dev)
+    _need(count.dtype == torch.int64 and count.numel() == 1 and count.device == dev, "count: CUDA int64 scalar")
+    _check(lib().gh_distill_count(_ptr(teacher_index), _ptr(teacher_logits), B, K, int(V), _ptr(count),
+                                  _stream_handle(stream)), "gh_distill_count")
+    return count
+
+
+@_on_device_of
+def gh_topk_distill(logits, teacher_index, teacher_logits, temperature: float = 1.0, renormalize: bool = True,
+                    reduction: str = "mean", *, with_grad: bool = True, n_valid_total=None, grad=None, loss=None,
+                    row_loss=None, stream=None):
+    """Distillation from a teacher's top logits: the loss and the logits gradient
+    (one call into ``gh_topk_distill``).
+
+    ``logits`` CUDA [B, V] float32 or bfloat16 with dense rows; ``teacher_index``
+    int64 and ``teacher_logits`` float32 [B, K], K <= 128, as ``gh_token_logprobs``
+    returns them (an id of -1 or a value of -inf is no entry).  The teacher's
+    probabilities are the softmax of the entries' ``value / temperature``, or,
+    with ``renormalize=False``, ``exp(value)``.  The loss is ``temperature**2``
+    times the rows' sum q (log q - log p), divided for "mean" by the number of
+    rows with an entry (or by ``n_valid_total``, a CUDA int64 scalar).  ``grad``
+    may be ``logits`` itself; ``row_loss`` (optional float32 [B]) is written when
+    given.  Returns ``(loss, grad)``; ``grad`` is None for ``with_grad=False``.
+    """
+    import torch
+    B, V, ld, dtype = _rows(logits)
+    dev = logits.device
+    _need(teacher_index.dim() == 2, "teacher_index: [B, K]")
+    K = teacher_index.shape[1]
+    _row_tensor(teacher_index, "teacher_index", torch.int64, (B, K), dev)
+    _row_tensor(teacher_logits, "teacher_logits", torch.float32, (B, K), dev)
+    _need(reduction in GH_REDUCTION, "reduction must be 'mean' or 'sum'")
+    ldg = ld
+    if with_grad:
+        grad, ldg = _grad_like(grad, logits, B, V, ld)
+    else:
+        _need(grad is None, "grad needs with_grad")
+    if loss is None:
+        loss = torch.empty((), dtype=torch.float32, device=dev)
+    _need(loss.dtype == torch.float32 and loss.numel() == 1 and loss.device == dev, "loss must be a float32 scalar")
+    if row_loss is not None:
+        _row_tensor(row_loss, "row_loss", torch.float32, (B,), dev)
+    if n_valid_total is not None:
+        _need(n_valid_total.dtype == torch.int64 and n_valid_total.numel() == 1 and n_valid_total.device == dev,
+              "n_valid_total: CUDA int64 scalar")
+    st = lib().gh_topk_distill(_ptr(logits), ld, _ptr(teacher_index), _ptr(teacher_logits), B, V, K, dtype,
+                               float(temperature), 1 if renormalize else 0, GH_REDUCTION[reduction],
+                               _ptr(n_valid_total), _ptr(loss), _ptr(row_loss), _ptr(grad), ldg,
+                               _stream_handle(stream))
+    _check(st, "gh_topk_distill")
+    return loss, grad
+
+
 def gh_linear_ce(inputs, weight, targets, ignore_index: int = -100, reduction: str = "mean",
                  z_loss: float = 0.0, chunk: int = 0, accum: str = "fp32", *, grad_inputs=None,
                  grad_weight=None, loss=None, stream=None):
@@ -545,7 +752,8 @@ def gh_linear_ce(inputs, weight, targets, ignore_index: int = -100, reduction: s
     return loss, grad_inputs, grad_weight
 
 
-GH_KERNEL = {"ce_row": 0, "logits_gemm": 1, "chunk_ce": 2, "dx_gemm": 3, "dw_gemm": 4, "ce_vjp": 5}
+GH_KERNEL = {"ce_row": 0, "logits_gemm": 1, "chunk_ce": 2, "dx_gemm": 3, "dw_gemm": 4, "ce_vjp": 5,
+             "logprobs": 6, "logprobs_vjp": 7, "distill": 8}
 
 
 def gh_profile_enable(enable: bool = True) -> None:
@@ -599,6 +807,7 @@ __all__ = [
     "GhError", "lib", "header_symbols", "status_string", "gh_status_string", "gh_version",
     "gh_ce_fwd_bwd", "gh_ce_fwd_bwd_noalloc", "GH_NOALLOC_MAX_ROWS", "gh_ce_fwd", "gh_selective_log_softmax",
     "gh_ce_vjp", "gh_linear_ce", "gh_chunked_linear_loss", "CHUNK_LOSS_FN",
+    "gh_token_logprobs", "gh_token_logprobs_vjp", "gh_topk_distill", "gh_distill_count", "GH_MAX_TOP_K",
     "gh_count_valid", "gh_ce_fwd_bwd_shard", "gh_linear_ce_shard", "gh_linear_ce_shard_f32",
     "gh_cast_f32_to_bf16", "gh_exp2_eval",
     "gh_get_device_status", "gh_profile_enable", "gh_profile_read", "gh_debug_set", "GH_DEBUG",

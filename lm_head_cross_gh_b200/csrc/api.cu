@@ -9,6 +9,7 @@
 #include "common.cuh"
 #include "linear_ce.h"
 #include "profile.h"
+#include "token_ops.h"
 
 namespace gh {
 
@@ -232,6 +233,150 @@ gh_status_t gh_selective_log_softmax(const void* logits, const int64_t* index, i
   a.mode = kModeSelect;
   a.profile_kind = GH_KERNEL_CE_ROW;
   return ce_launch(a, rows, dtype, static_cast<cudaStream_t>(stream_));
+}
+
+// Temperatures the token operators take: far inside this range 1 / T and
+// log2(e) / T times any logit's distance from its row's maximum stay finite.
+static bool temperature_ok(float t) { return t >= 1e-4f && t <= 1e4f; }
+
+// A [B, V] output with its own row stride may be the input itself or lie apart from it.
+static bool aliases_partly(const void* in, int64_t ld, const void* out, int64_t ld_out, int64_t B, int64_t V, int es) {
+  if (in == out && ld == ld_out) return false;
+  const uintptr_t i0 = reinterpret_cast<uintptr_t>(in), o0 = reinterpret_cast<uintptr_t>(out);
+  const uintptr_t ib = (static_cast<uintptr_t>(B - 1) * ld + V) * es, ob = (static_cast<uintptr_t>(B - 1) * ld_out + V) * es;
+  return i0 < o0 + ob && o0 < i0 + ib;
+}
+
+static bool misaligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
+gh_status_t gh_token_logprobs(const void* logits, int64_t ld, const int64_t* index, int64_t B, int64_t V,
+                              gh_dtype_t dtype, int64_t ignore_index, float temperature, int64_t top_k,
+                              float* logprob, float* entropy, float* lse, float* top_logprob, int64_t* top_index,
+                              void* stream) {
+  if (B < 0 || V < 1 || V >= (int64_t(1) << 31) || ld < V || top_k < 0 || top_k > V) return GH_ERR_INVALID_ARG;
+  if (dtype != GH_F32 && dtype != GH_BF16) return GH_ERR_INVALID_ARG;
+  if (!temperature_ok(temperature)) return GH_ERR_INVALID_ARG;
+  if (top_k > GH_MAX_TOP_K) return GH_ERR_UNSUPPORTED;
+  if (B > 0 && (!logits || !index || !logprob || !entropy || !lse)) return GH_ERR_INVALID_ARG;
+  if (B > 0 && top_k > 0 && (!top_logprob || !top_index)) return GH_ERR_INVALID_ARG;
+  const int es = dtype == GH_F32 ? 4 : 2;
+  if (misaligned(logits, es) || misaligned(index, 8) || misaligned(logprob, 4) || misaligned(entropy, 4) ||
+      misaligned(lse, 4) || (top_k > 0 && (misaligned(top_logprob, 4) || misaligned(top_index, 8))))
+    return GH_ERR_INVALID_ARG;
+  if (B == 0) return GH_OK;
+  LogprobArgs a{};
+  a.logits = logits;
+  a.index = index;
+  a.B = B;
+  a.V = V;
+  a.ld = ld;
+  a.ignore_index = ignore_index;
+  a.c = static_cast<float>(1.4426950408889634 / static_cast<double>(temperature));
+  a.top_k = static_cast<int>(top_k);
+  a.logprob = logprob;
+  a.entropy = entropy;
+  a.lse = lse;
+  a.top_logprob = top_logprob;
+  a.top_index = top_index;
+  return logprobs_launch(a, dtype, static_cast<cudaStream_t>(stream));
+}
+
+gh_status_t gh_token_logprobs_vjp(const void* logits, int64_t ld, const int64_t* index, int64_t B, int64_t V,
+                                  gh_dtype_t dtype, int64_t ignore_index, float temperature, const float* lse,
+                                  const float* entropy, const float* g_logprob, const float* g_entropy, void* grad,
+                                  int64_t ld_grad, void* stream) {
+  if (B < 0 || V < 1 || V >= (int64_t(1) << 31) || ld < V || ld_grad < V) return GH_ERR_INVALID_ARG;
+  if (dtype != GH_F32 && dtype != GH_BF16) return GH_ERR_INVALID_ARG;
+  if (!temperature_ok(temperature)) return GH_ERR_INVALID_ARG;
+  if (B > 0 && (!logits || !index || !lse || !entropy || !g_logprob || !grad)) return GH_ERR_INVALID_ARG;
+  const int es = dtype == GH_F32 ? 4 : 2;
+  if (misaligned(logits, es) || misaligned(grad, es) || misaligned(index, 8) || misaligned(lse, 4) ||
+      misaligned(entropy, 4) || misaligned(g_logprob, 4) || misaligned(g_entropy, 4))
+    return GH_ERR_INVALID_ARG;
+  if (B > 0 && aliases_partly(logits, ld, grad, ld_grad, B, V, es)) return GH_ERR_INVALID_ARG;
+  if (B == 0) return GH_OK;
+  LogprobVjpArgs a{};
+  a.logits = logits;
+  a.grad = grad;
+  a.index = index;
+  a.B = B;
+  a.V = V;
+  a.ld = ld;
+  a.ld_grad = ld_grad;
+  a.ignore_index = ignore_index;
+  const double c = 1.4426950408889634 / static_cast<double>(temperature);
+  a.c = static_cast<float>(c);
+  a.c_lo = static_cast<float>(c - static_cast<double>(a.c));
+  a.inv_t = static_cast<float>(1.0 / static_cast<double>(temperature));
+  a.lse = lse;
+  a.entropy = entropy;
+  a.g_logprob = g_logprob;
+  a.g_entropy = g_entropy;
+  return logprobs_vjp_launch(a, dtype, static_cast<cudaStream_t>(stream));
+}
+
+gh_status_t gh_distill_count(const int64_t* teacher_index, const float* teacher_logits, int64_t B, int64_t K,
+                             int64_t V, int64_t* count, void* stream_) {
+  if (B < 0 || V < 1 || V >= (int64_t(1) << 31) || K < 1 || !count || misaligned(count, 8)) return GH_ERR_INVALID_ARG;
+  if (K > GH_MAX_TOP_K) return GH_ERR_UNSUPPORTED;
+  if (B > 0 && (!teacher_index || !teacher_logits)) return GH_ERR_INVALID_ARG;
+  if (misaligned(teacher_index, 8) || misaligned(teacher_logits, 4)) return GH_ERR_INVALID_ARG;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (B == 0) return cudaMemsetAsync(count, 0, sizeof(int64_t), stream) == cudaSuccess ? GH_OK : GH_ERR_CUDA;
+  return distill_count_launch(teacher_index, teacher_logits, B, static_cast<int>(K), V,
+                              reinterpret_cast<unsigned long long*>(count), stream);
+}
+
+gh_status_t gh_topk_distill(const void* logits, int64_t ld, const int64_t* teacher_index,
+                            const float* teacher_logits, int64_t B, int64_t V, int64_t K, gh_dtype_t dtype,
+                            float temperature, int renormalize, gh_reduction_t reduction,
+                            const int64_t* n_valid_total, float* loss, float* row_loss_out, void* grad,
+                            int64_t ld_grad, void* stream_) {
+  if (B < 0 || V < 1 || V >= (int64_t(1) << 31) || K < 1 || ld < V || (grad && ld_grad < V)) return GH_ERR_INVALID_ARG;
+  if (dtype != GH_F32 && dtype != GH_BF16) return GH_ERR_INVALID_ARG;
+  if (!temperature_ok(temperature) || (renormalize != 0 && renormalize != 1)) return GH_ERR_INVALID_ARG;
+  if (reduction != GH_REDUCTION_MEAN && reduction != GH_REDUCTION_SUM) return GH_ERR_INVALID_ARG;
+  if (K > GH_MAX_TOP_K) return GH_ERR_UNSUPPORTED;
+  if (!loss || (B > 0 && (!logits || !teacher_index || !teacher_logits))) return GH_ERR_INVALID_ARG;
+  const int es = dtype == GH_F32 ? 4 : 2;
+  if (misaligned(logits, es) || misaligned(grad, es) || misaligned(teacher_index, 8) || misaligned(teacher_logits, 4) ||
+      misaligned(loss, 4) || misaligned(row_loss_out, 4) || misaligned(n_valid_total, 8))
+    return GH_ERR_INVALID_ARG;
+  if (B > 0 && grad && aliases_partly(logits, ld, grad, ld_grad, B, V, es)) return GH_ERR_INVALID_ARG;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (B == 0) return cudaMemsetAsync(loss, 0, sizeof(float), stream) == cudaSuccess ? GH_OK : GH_ERR_CUDA;
+
+  // Scratch: the count, and the row losses unless the caller takes them.
+  void* scratch = nullptr;
+  const size_t rows_bytes = row_loss_out ? 0 : static_cast<size_t>(B) * sizeof(float);
+  gh_status_t st = scratch_alloc(&scratch, 16 + rows_bytes, stream);
+  if (st != GH_OK) return st;
+  unsigned long long* counter = static_cast<unsigned long long*>(scratch);
+  float* row_loss = row_loss_out ? row_loss_out : reinterpret_cast<float*>(static_cast<char*>(scratch) + 16);
+  const unsigned long long* n_valid =
+      n_valid_total ? reinterpret_cast<const unsigned long long*>(n_valid_total) : counter;
+  const int mean = reduction == GH_REDUCTION_MEAN;
+  DistillArgs a{};
+  a.logits = logits;
+  a.grad = grad;
+  a.B = B;
+  a.V = V;
+  a.ld = ld;
+  a.ld_grad = ld_grad;
+  a.ids = teacher_index;
+  a.values = teacher_logits;
+  a.K = static_cast<int>(K);
+  a.temperature = temperature;
+  a.c = static_cast<float>(1.4426950408889634 / static_cast<double>(temperature));
+  a.renormalize = renormalize;
+  a.mean = mean;
+  a.n_valid = n_valid;
+  a.row_loss = row_loss;
+  if (!n_valid_total) st = distill_count_launch(teacher_index, teacher_logits, B, a.K, V, counter, stream);
+  if (st == GH_OK) st = distill_launch(a, dtype, stream);
+  if (st == GH_OK) st = ce_reduce_launch(row_loss, B, n_valid, mean, loss, stream);
+  scratch_free(scratch, stream);
+  return st;
 }
 
 static gh_status_t linear_ce_impl(const void* inputs, const void* weight, const int64_t* targets, int64_t N,

@@ -3,6 +3,8 @@
 #include "ce.cu"
 #include "ce_ring.cu"
 #include "ce_vjp.cu"
+#include "token_logprobs.cu"
+#include "topk_distill.cu"
 #include "linear_ce.cu"
 #include "api.cu"
 #include "noalloc.cu"

@@ -1,0 +1,59 @@
+// Internal interface of the token log-probability kernels (token_logprobs.cu)
+// and the top-logits distillation kernels (topk_distill.cu).
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "../../include/gh.h"
+
+namespace gh {
+
+struct LogprobArgs {
+  const void* logits;    // [B, V], row stride ld elements
+  const int64_t* index;  // [B]
+  int64_t B, V, ld;
+  int64_t ignore_index;
+  float c;               // log2(e) / temperature
+  int top_k;
+  float* logprob;        // [B]
+  float* entropy;        // [B]
+  float* lse;            // [B], of the scaled logits
+  float* top_logprob;    // [B, top_k]
+  int64_t* top_index;    // [B, top_k]
+};
+
+struct LogprobVjpArgs {
+  const void* logits;  // [B, V], row stride ld
+  void* grad;          // [B, V], row stride ld_grad (may be logits with the same stride)
+  const int64_t* index;
+  int64_t B, V, ld, ld_grad;
+  int64_t ignore_index;
+  float c, c_lo;  // log2(e) / temperature as a sum of two floats
+  float inv_t;    // 1 / temperature
+  const float *lse, *entropy, *g_logprob, *g_entropy;  // [B] (g_entropy may be null)
+};
+
+struct DistillArgs {
+  const void* logits;
+  void* grad;  // null: loss only
+  int64_t B, V, ld, ld_grad;
+  const int64_t* ids;   // [B, K] teacher entries
+  const float* values;  // [B, K]
+  int K;
+  float temperature;
+  float c;       // log2(e) / temperature
+  int renormalize;
+  int mean;
+  const unsigned long long* n_valid;  // rows with an entry (of the whole batch)
+  float* row_loss;                    // [B]
+};
+
+gh_status_t logprobs_launch(const LogprobArgs& a, gh_dtype_t dtype, cudaStream_t stream);
+gh_status_t logprobs_vjp_launch(const LogprobVjpArgs& a, gh_dtype_t dtype, cudaStream_t stream);
+// Counts the rows with an entry into *count (written, not added to).
+gh_status_t distill_count_launch(const int64_t* ids, const float* values, int64_t B, int K, int64_t V,
+                                 unsigned long long* count, cudaStream_t stream);
+gh_status_t distill_launch(const DistillArgs& a, gh_dtype_t dtype, cudaStream_t stream);
+
+}  // namespace gh

@@ -14,6 +14,9 @@ the tensors: there is no other implementation behind these functions.
 * ``autograd_loss_and_logits_grad(loss_fn)``: adapts a PyTorch scalar loss to
   the ``(loss, grad_logits)`` contract of ``chunked_linear_loss``
 * ``selective_log_softmax(logits, index)`` (forward only)
+* ``token_logprobs(logits, index, top_k, temperature, ignore_index)``,
+  ``topk_distillation(logits, teacher_index, teacher_logits, ...)`` and its linear
+  form ``chunked_linear_topk_distillation`` (no Greyhound counterparts)
 
 Data parallel (one process per GPU, a batch split over the ranks of a
 ``torch.distributed`` group):
@@ -29,12 +32,14 @@ from __future__ import annotations
 
 import torch
 
-from . import (gh_ce_fwd, gh_ce_fwd_bwd, gh_chunked_linear_loss, gh_linear_ce, gh_selective_log_softmax)
+from . import (gh_ce_fwd, gh_ce_fwd_bwd, gh_chunked_linear_loss, gh_distill_count, gh_linear_ce,
+               gh_selective_log_softmax, gh_token_logprobs, gh_token_logprobs_vjp, gh_topk_distill)
 
 _PKG = __name__.rpartition(".")[0]
 
 __all__ = ["cross_entropy", "chunked_linear_cross_entropy", "chunked_linear_loss",
-           "autograd_loss_and_logits_grad", "selective_log_softmax", "data_parallel_cross_entropy",
+           "autograd_loss_and_logits_grad", "selective_log_softmax", "token_logprobs", "topk_distillation",
+           "chunked_linear_topk_distillation", "data_parallel_cross_entropy",
            "data_parallel_chunked_linear_cross_entropy"]
 
 
@@ -144,6 +149,100 @@ def autograd_loss_and_logits_grad(loss_fn):
 def selective_log_softmax(logits, index):
     """``log_softmax(logits)`` gathered at ``index`` (forward only): float32 [...]."""
     return gh_selective_log_softmax(logits.contiguous(), index.contiguous())
+
+
+def _dense_rows(logits):
+    """[..., V] logits as [rows, V] with dense rows (a copy only where the layout needs one)."""
+    x = logits if logits.dim() == 2 else logits.reshape(-1, logits.shape[-1])
+    if x.shape[1] > 1 and (x.stride(1) != 1 or (x.shape[0] > 1 and x.stride(0) < x.shape[1])):
+        x = x.contiguous()
+    return x
+
+
+class _TokenLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, index, top_k, temperature, ignore_index):
+        x = _dense_rows(logits)
+        t = index.reshape(-1).contiguous()
+        logprob, entropy, lse, top_logprob, top_index = gh_token_logprobs(x, t, top_k, temperature, ignore_index)
+        ctx.save_for_backward(x, t, lse, entropy)
+        ctx.conf = (logits.shape, temperature, ignore_index)
+        lead = logits.shape[:-1]
+        logprob, entropy = logprob.view(lead), entropy.clone().view(lead)
+        if top_logprob is None:
+            return logprob, entropy
+        top_logprob, top_index = top_logprob.view(*lead, -1), top_index.view(*lead, -1)
+        ctx.mark_non_differentiable(top_logprob, top_index)
+        return logprob, entropy, top_logprob, top_index
+
+    @staticmethod
+    def backward(ctx, g_logprob, g_entropy, *unused):
+        x, t, lse, entropy = ctx.saved_tensors
+        shape, temperature, ignore_index = ctx.conf
+        grad = gh_token_logprobs_vjp(x, t, lse, entropy, g_logprob.reshape(-1).float().contiguous(),
+                                     g_entropy.reshape(-1).float().contiguous(), temperature, ignore_index)
+        return grad.reshape(shape), None, None, None, None
+
+
+def token_logprobs(logits, index, top_k: int = 0, temperature: float = 1.0, ignore_index: int = -100):
+    """Log-probabilities of ``index`` [...] under ``logits`` [..., V] (float32 or
+    bfloat16, CUDA) over ``temperature``, and the rows' entropies: float32 [...]
+    each, both differentiable.  With ``top_k`` also the most probable
+    alternatives' log-probabilities (float32) and ids (int64) [..., top_k], which
+    carry no gradient.  Rows whose index is ``ignore_index`` give 0, 0, -inf and
+    -1 and a zero gradient."""
+    return _TokenLogprobs.apply(logits, index, int(top_k), float(temperature), int(ignore_index))
+
+
+class _TopkDistillation(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, teacher_index, teacher_logits, temperature, renormalize, reduction):
+        x = _dense_rows(logits)
+        K = teacher_index.shape[-1]
+        ids = teacher_index.reshape(-1, K).contiguous()
+        values = teacher_logits.reshape(-1, K).float().contiguous()
+        ctx.shape = logits.shape
+        loss, grad = gh_topk_distill(x, ids, values, temperature, renormalize, reduction,
+                                     with_grad=ctx.needs_input_grad[0])
+        if grad is not None:
+            ctx.save_for_backward(grad)
+        return loss
+
+    @staticmethod
+    def backward(ctx, g):
+        (grad,) = ctx.saved_tensors
+        return _scaled(grad, g).reshape(ctx.shape), None, None, None, None, None
+
+
+def topk_distillation(logits, teacher_index, teacher_logits, temperature: float = 1.0, renormalize: bool = True,
+                      reduction: str = "mean"):
+    """Distillation of ``logits`` [..., V] (float32 or bfloat16, CUDA) from a
+    teacher's stored entries ``teacher_index`` (int64) and ``teacher_logits``
+    [..., K]: ``temperature**2`` times the Kullback-Leibler sum over the entries
+    (see ``gh_topk_distill``).  Returns a float32 scalar; its backward gives the
+    logits gradient computed in the forward pass (the teacher gets none)."""
+    return _TopkDistillation.apply(logits, teacher_index, teacher_logits, float(temperature), bool(renormalize),
+                                   reduction)
+
+
+def chunked_linear_topk_distillation(inputs, weight, teacher_index, teacher_logits, temperature: float = 1.0,
+                                     renormalize: bool = True, reduction: str = "mean", chunk_size=None,
+                                     grad_weight_accum_dtype: str = "fp32"):
+    """``topk_distillation`` of ``inputs @ weight.T`` (bf16 [BT, D] and [V, D],
+    CUDA) in row chunks without materialising the logits (``chunked_linear_loss``
+    with the distillation in place on each chunk): ``teacher_index`` and
+    ``teacher_logits`` are [BT, K]; a mean divides by all chunks' rows with an
+    entry.  The chunk logits are bf16, as for any ``chunked_linear_loss``."""
+    ids = teacher_index.contiguous()
+    values = teacher_logits.float().contiguous()
+    total = gh_distill_count(ids, values, weight.shape[0])
+
+    def loss_and_grad(logits, ids, values):
+        return gh_topk_distill(logits, ids, values, temperature, renormalize, reduction, n_valid_total=total,
+                               grad=logits)
+
+    return chunked_linear_loss(inputs, weight, loss_and_grad, ids, values, chunk_size=chunk_size,
+                               grad_weight_accum_dtype=grad_weight_accum_dtype)
 
 
 def _ops(ops):

@@ -37,6 +37,7 @@ from .ce import (bf16_round, cross_entropy, ce_rows, ce_vjp, n_valid_and_scale,
                  selective_log_softmax)
 from .linear_ce import (grad_input_rows, grad_weight_rows, linear_cross_entropy,
                         linear_cross_entropy_materialised, loss_from_lse, row_lse)
+from .token_ops import token_logprobs, token_logprobs_vjp, topk_distill
 
 __all__ = [
     "bf16_round",
@@ -51,4 +52,7 @@ __all__ = [
     "loss_from_lse",
     "grad_input_rows",
     "grad_weight_rows",
+    "token_logprobs",
+    "token_logprobs_vjp",
+    "topk_distill",
 ]

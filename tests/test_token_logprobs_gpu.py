@@ -1,0 +1,306 @@
+"""GPU parity of gh_token_logprobs and gh_token_logprobs_vjp against the float64
+oracle (tolerances: token_ops_check)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import lm_head_cross_gh_b200 as gh
+from lm_head_cross_gh_b200 import functional as GF
+from token_ops_check import check_logprobs, check_vjp, logits
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = [torch.float32, torch.bfloat16]
+
+
+def given(B, V, seed, ignored=0.2):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    t = torch.randint(0, V, (B,), generator=g, device="cuda")
+    t[torch.rand(B, generator=g, device="cuda") < ignored] = -100
+    return t
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V", [1, 2, 7, 8, 9, 31, 63, 64, 65, 129, 1023, 1025, 4099, 8191, 8193, 50257])
+def test_sizes(cuda_device, dtype, V):
+    B = 11 if V < 9000 else 5
+    for k, T, pad in ((0, 1.0, 0), (min(V, 1), 0.7, 3), (min(V, 20), 2.0, 0), (min(V, 128), 1.0, 5)):
+        x, t = logits(B, V, dtype, V + k, pad), given(B, V, V + k)
+        out = gh.gh_token_logprobs(x, t, k, T)
+        check_logprobs(x, t, k, T, out, what=f"{dtype} V={V} k={k} T={T} pad={pad}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B,V,k", [(1, 50257, 20), (2, 262144, 128), (150, 5003, 64), (300, 1000, 5),
+                                   (1300, 2003, 33), (2500, 131, 128), (1200, 8200, 20)])
+def test_batches(cuda_device, dtype, B, V, k):
+    x, t = logits(B, V, dtype, B), given(B, V, B)
+    out = gh.gh_token_logprobs(x, t, k, 1.3)
+    check_logprobs(x, t, k, 1.3, out, what=f"{dtype} {B}x{V}")
+    again = gh.gh_token_logprobs(x, t, k, 1.3)
+    for a, b in zip(out, again):
+        assert torch.equal(a, b), "two calls differ"
+
+
+def test_long_rows_of_a_few_tokens(cuda_device):
+    # rows far longer than any vocabulary: still one answer per row
+    x, t = logits(3, 3_000_001, torch.bfloat16, 1, sigma=2.0), given(3, 3_000_001, 1, 0.0)
+    check_logprobs(x, t, 40, 1.0, gh.gh_token_logprobs(x, t, 40))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B", [6, 1250])
+def test_ties_go_to_the_lowest_index(cuda_device, dtype, B):
+    V = 3001
+    x = logits(B, V, dtype, 3).round()  # a few dozen distinct values
+    x[0] = 0.25                          # all alike
+    x[1] = torch.arange(V, device="cuda").to(dtype)          # rising (bf16: runs of equal values)
+    x[2] = -torch.arange(V, device="cuda").to(dtype)
+    x[3] = torch.where(torch.arange(V, device="cuda") % 2 == 0, 0.0, -0.0).to(dtype)  # both zeros are one value
+    x[4] = -5.0
+    x[4, -60:] = 7.0
+    t = given(B, V, 4, 0.0)
+    for k in (1, 20, 128):
+        check_logprobs(x, t, k, 1.0, gh.gh_token_logprobs(x, t, k), what=f"k={k}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B", [7, 1250])
+def test_masked_and_non_finite_logits(cuda_device, dtype, B):
+    V, k = 2053, 20
+    low = torch.finfo(dtype).min
+    x = logits(B, V, dtype, 5)
+    t = given(B, V, 6, 0.0)
+    x[0, 3:] = -math.inf                 # fewer tokens than alternatives
+    x[1] = -math.inf                     # nothing left: no distribution
+    x[2] = low                           # a mask of the lowest value that leaves nothing: uniform
+    x[3, ::2] = low
+    x[4, 100] = math.nan
+    x[5, 2000] = math.inf
+    x[6, : V - 1] = -math.inf            # one token left
+    if B > 10:
+        x[7] = low
+        x[7, 5:900] = -math.inf          # lowest values and -inf: uniform over the former
+        x[8] = -1000.0
+        x[9] = x[9] * 50.0
+    check_logprobs(x, t, k, 1.0, gh.gh_token_logprobs(x, t, k), what="T=1")
+    check_logprobs(x, t, k, 0.5, gh.gh_token_logprobs(x, t, k, 0.5), what="T=0.5")
+    # the gradient: zero at masked logits, NaN rows where there is no distribution
+    for T in (1.0, 0.5):
+        lp, ent, lse, _, _ = gh.gh_token_logprobs(x, t, 0, T)
+        gl, gH = torch.randn(B, device="cuda"), torch.randn(B, device="cuda")
+        grad = gh.gh_token_logprobs_vjp(x, t, lse, ent, gl, gH, T)
+        assert torch.isnan(grad[[1, 4, 5]]).all()
+        keep = [r for r in range(B) if r not in (1, 4, 5)]
+        gone = torch.isneginf(x[keep]) & (torch.arange(V, device="cuda")[None] != t[keep][:, None])
+        assert not grad[keep][gone].any()
+        check_vjp(x[keep], t[keep], gl[keep], gH[keep], T, grad[keep], what=f"vjp T={T}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B", [3, 1250])
+@pytest.mark.parametrize("T", [0.5, 1.0, 3.0])
+def test_rows_far_from_zero_keep_their_distribution(cuda_device, dtype, B, T):
+    """All logits at one value far below 0 (a mask that leaves nothing): the
+    uniform distribution, in closed form.  2^-20 relative covers log2 and the
+    few roundings; the row constant is exact because every difference is 0."""
+    V = 1537
+    x = logits(B, V, dtype, 51)
+    t = given(B, V, 52, 0.0)
+    for r, low in enumerate((torch.finfo(dtype).min, -1e9, -3e4)):
+        x[r] = low
+    lp, ent, lse, top, ids = gh.gh_token_logprobs(x, t, 3, T)
+    want = torch.full((3,), math.log(V), device="cuda")
+    assert torch.allclose(lp[:3], -want, rtol=2.0 ** -20, atol=0)
+    assert torch.allclose(ent[:3], want, rtol=2.0 ** -20, atol=0)
+    assert torch.allclose(top[:3], -want[:, None].expand(3, 3), rtol=2.0 ** -20, atol=0)
+    assert (ids[:3] == torch.arange(3, device="cuda")).all()
+    gl, gH = torch.full((B,), 2.0, device="cuda"), torch.full((B,), 3.0, device="cuda")
+    grad = gh.gh_token_logprobs_vjp(x, t, lse, ent, gl, gH, T)[:3].float()
+    expect = torch.full((3, V), -2.0 / V / T, device="cuda")
+    expect[torch.arange(3), t[:3]] += 2.0 / T
+    # the entropy's part is 3 p (log p + H) / T = 0 up to the rounding of log p + H (2^-19 log V)
+    tol = expect.abs() * (torch.finfo(dtype).eps / 2 + 2.0 ** -18) + 3.0 * math.log(V) * 2.0 ** -19 / V / T
+    assert ((grad - expect).abs() <= tol).all()
+
+
+def test_extreme_temperatures(cuda_device):
+    x, t = logits(9, 777, torch.float32, 7), given(9, 777, 7)
+    for T in (1e-4, 1e4):
+        check_logprobs(x, t, 9, T, gh.gh_token_logprobs(x, t, 9, T), what=f"T={T}")
+
+
+def test_index_out_of_range_and_ignore_index_inside_the_vocabulary(cuda_device):
+    gh.gh_get_device_status()
+    x = logits(4, 300, torch.bfloat16, 8)
+    t = torch.tensor([5, 300, 7, -3], device="cuda")
+    out = gh.gh_token_logprobs(x, t, 4)
+    torch.cuda.synchronize()
+    assert gh.gh_get_device_status() == gh.GH_ERR_TARGET_RANGE
+    for v in out[:4]:
+        assert torch.isnan(v[[1, 3]]).all()
+    assert (out[4][[1, 3]] == -1).all()
+    check_logprobs(x[[0, 2]], t[[0, 2]], 4, 1.0, [v[[0, 2]] for v in out])
+    g = gh.gh_token_logprobs_vjp(x, t, out[2], out[1], torch.ones(4, device="cuda"))
+    assert gh.gh_get_device_status() == gh.GH_ERR_TARGET_RANGE
+    assert not g[[1, 3]].any()
+    t = torch.tensor([5, 5, 7, 5], device="cuda")
+    check_logprobs(x, t, 3, 1.0, gh.gh_token_logprobs(x, t, 3, 1.0, 5), ignore_index=5)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V", [1, 2, 7, 8, 9, 100, 1023, 1025, 8191, 50257])
+def test_vjp_sizes(cuda_device, dtype, V):
+    B = 37 if V < 20000 else 9
+    for T, pad, with_h in ((1.0, 0, True), (0.6, 3, True), (2.0, 0, False)):
+        x, t = logits(B, V, dtype, V, pad), given(B, V, V)
+        _, ent, lse, _, _ = gh.gh_token_logprobs(x, t, 0, T)
+        gl = torch.randn(B, device="cuda")
+        gH = torch.randn(B, device="cuda") if with_h else None
+        gl[::5] = 0.0
+        grad = gh.gh_token_logprobs_vjp(x, t, lse, ent, gl, gH, T)
+        check_vjp(x, t, gl, gH, T, grad, what=f"{dtype} V={V} T={T}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_vjp_in_place_other_phase_and_untouched_padding(cuda_device, dtype):
+    B, V = 40, 3001
+    x, t = logits(B, V, dtype, 11, pad=7), given(B, V, 11)
+    _, ent, lse, _, _ = gh.gh_token_logprobs(x, t)
+    gl, gH = torch.randn(B, device="cuda"), torch.randn(B, device="cuda")
+    want = gh.gh_token_logprobs_vjp(x, t, lse, ent, gl, gH)
+    check_vjp(x, t, gl, gH, 1.0, want)
+    buf = torch.full((B * 3050 + 16,), 9.0, dtype=dtype, device="cuda")
+    shifted = buf[3:3 + B * 3050].view(B, 3050)[:, :V]   # another 16-byte phase and row stride
+    gh.gh_token_logprobs_vjp(x, t, lse, ent, gl, gH, grad=shifted)
+    assert torch.equal(shifted, want)
+    rest = buf.clone()
+    rest[3:3 + B * 3050].view(B, 3050)[:, :V] = 9.0
+    assert (rest == 9.0).all(), "wrote outside the gradient"
+    whole = torch.full((B, V + 7), 9.0, dtype=dtype, device="cuda")
+    whole[:, :V] = x
+    y = whole[:, :V]
+    gh.gh_token_logprobs_vjp(y, t, lse, ent, gl, gH, grad=y)
+    assert torch.equal(y, want) and (whole[:, V:] == 9.0).all()
+
+
+def test_vjp_many_rows(cuda_device):
+    x, t = logits(1500, 5003, torch.bfloat16, 12), given(1500, 5003, 12)
+    _, ent, lse, _, _ = gh.gh_token_logprobs(x, t)
+    gl, gH = torch.randn(1500, device="cuda"), torch.randn(1500, device="cuda")
+    check_vjp(x, t, gl, gH, 1.0, gh.gh_token_logprobs_vjp(x, t, lse, ent, gl, gH))
+
+
+def test_offsets_beyond_32_bits(cuda_device):
+    B, V = 17000, 131072  # 2.2e9 logits
+    x = torch.zeros(B, V, dtype=torch.bfloat16, device="cuda")
+    tail = logits(8, V, torch.bfloat16, 13)
+    x[-8:] = tail
+    t = torch.full((B,), -100, dtype=torch.int64, device="cuda")
+    t[-8:] = given(8, V, 13, 0.0)
+    out = gh.gh_token_logprobs(x, t, 16)
+    check_logprobs(tail, t[-8:], 16, 1.0, [v[-8:] for v in out])
+    gl = torch.ones(B, device="cuda")
+    g = gh.gh_token_logprobs_vjp(x, t, out[2], out[1], gl, gl, grad=x)
+    check_vjp(tail, t[-8:], gl[-8:], gl[-8:], 1.0, g[-8:])
+    assert not g[:-8].any()
+
+
+def test_empty_batch(cuda_device):
+    x, t = torch.empty(0, 5, device="cuda"), torch.empty(0, dtype=torch.int64, device="cuda")
+    lp, ent, lse, top, ids = gh.gh_token_logprobs(x, t, 2)
+    assert lp.shape == ent.shape == lse.shape == (0,) and top.shape == ids.shape == (0, 2)
+    z = torch.empty(0, device="cuda")
+    assert gh.gh_token_logprobs_vjp(x, t, z, z, z).shape == (0, 5)
+
+
+@pytest.mark.parametrize("B,V", [(3, 50257), (1300, 2003)])
+def test_captured_graphs_and_streams(cuda_device, B, V):
+    # two graphs of the same call on other inputs, replayed in turn and on two streams
+    k = 20
+    xs = [logits(B, V, torch.bfloat16, s) for s in (21, 22)]
+    ts = [given(B, V, s) for s in (21, 22)]
+    want = [gh.gh_token_logprobs(x, t, k) for x, t in zip(xs, ts)]
+    graphs, outs = [], []
+    side = torch.cuda.Stream()
+    for x, t in zip(xs, ts):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(gh.gh_token_logprobs(x, t, k))
+        graphs.append(g)
+    for _ in range(3):
+        for o in outs:
+            for v in o:
+                v.zero_()
+        torch.cuda.synchronize()
+        graphs[0].replay()
+        with torch.cuda.stream(side):
+            graphs[1].replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            for a, b in zip(o, w):
+                assert torch.equal(a, b)
+    # two calls at once on two streams
+    with torch.cuda.stream(side):
+        a = gh.gh_token_logprobs(xs[0], ts[0], k)
+    b = gh.gh_token_logprobs(xs[1], ts[1], k)
+    torch.cuda.synchronize()
+    for o, w in zip((a, b), want):
+        assert all(torch.equal(p, q) for p, q in zip(o, w))
+
+
+def test_given_outputs_are_written_and_nothing_behind_them(cuda_device):
+    B, V, k = 13, 1001, 7
+    x, t = logits(B, V, torch.float32, 31), given(B, V, 31)
+    f = torch.full((4, B + 3), 5.0, device="cuda")
+    top, ids = torch.full((B + 2, k), 5.0, device="cuda"), torch.full((B + 2, k), 5, device="cuda")
+    out = gh.gh_token_logprobs(x, t, k, logprob=f[0, :B], entropy=f[1, :B], lse=f[2, :B], top_logprob=top[:B],
+                               top_index=ids[:B])
+    check_logprobs(x, t, k, 1.0, out)
+    assert (f[:3, B:] == 5.0).all() and (top[B:] == 5.0).all() and (ids[B:] == 5).all()
+
+
+def test_functional_gradients(cuda_device):
+    """Autograd against the formula (float64 autograd) and against differences."""
+    torch.manual_seed(1)
+    x = torch.randn(2, 3, 50, device="cuda", requires_grad=True)
+    t = torch.randint(0, 50, (2, 3), device="cuda")
+    t[0, 1] = -100
+    gl, gH = torch.randn(2, 3, device="cuda"), torch.randn(2, 3, device="cuda")
+    lp, ent, top, ids = GF.token_logprobs(x, t, 4, 0.8)
+    assert lp.shape == ent.shape == (2, 3) and top.shape == ids.shape == (2, 3, 4)
+    assert not top.requires_grad and not ids.requires_grad
+    (gl * lp + gH * ent).sum().backward()
+    y = x.detach().double().requires_grad_(True)
+
+    def value(z):
+        logp = torch.log_softmax(z / 0.8, dim=-1)
+        l = logp.gather(-1, t.clamp_min(0)[..., None])[..., 0]
+        h = -(logp.exp() * logp).sum(-1)
+        return ((gl * l + gH * h) * (t != -100)).sum()
+
+    value(y).backward()
+    assert torch.allclose(x.grad.double(), y.grad, rtol=1e-5, atol=1e-6)
+    d = torch.randn(2, 3, 50, device="cuda", dtype=torch.float64)
+    diff = (value(y.detach() + 1e-5 * d) - value(y.detach() - 1e-5 * d)) / 2e-5
+    assert abs((x.grad.double() * d).sum() - diff) < 1e-4
+    with torch.no_grad():
+        lp2, ent2 = GF.token_logprobs(x, t, temperature=0.8)
+    assert torch.equal(lp2, lp) and torch.equal(ent2, ent)
+    # a sequence dimension that is not dense, and a broadcast upstream gradient
+    xt = x.detach().transpose(0, 1)
+    assert torch.equal(GF.token_logprobs(xt, t.t(), temperature=0.8)[0], lp.t())
+    xb = x.detach().clone().requires_grad_(True)
+    GF.token_logprobs(xb, t, temperature=0.8)[0].sum().backward()
+    assert torch.allclose(xb.grad.sum(-1), torch.zeros(2, 3, device="cuda"), atol=1e-5)
+
+
+def test_selected_value_agrees_with_selective_log_softmax(cuda_device):
+    x, t = logits(200, 50257, torch.bfloat16, 41), given(200, 50257, 41, 0.0)
+    lp = gh.gh_token_logprobs(x, t)[0]
+    sel = gh.gh_selective_log_softmax(x, t)
+    eps = 4e-7 * max(1.0, float(x.abs().max()))
+    assert (lp - sel).abs().max().item() <= 4 * eps + 2.0 ** -21 * float(sel.abs().max())

@@ -1,0 +1,95 @@
+"""Refusals of the token operators' entry points, before anything reaches the
+GPU (no GPU needed)."""
+import pytest
+import torch
+
+import lm_head_cross_gh_b200 as gh
+
+FAKE = 0x7F0000000000  # a well-aligned non-null address; never dereferenced
+
+
+def at(k):
+    return FAKE + (k << 32)
+
+
+@pytest.fixture(scope="module")
+def L():
+    from lm_head_cross_gh_b200 import _build
+    _build.build()
+    return gh.lib()
+
+
+BAD, UNSUPPORTED = gh.GH_ERR_INVALID_ARG, gh.GH_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(B=-1), BAD), (dict(V=0), BAD), (dict(V=1 << 31, ld=1 << 31), BAD), (dict(ld=99), BAD), (dict(dtype=2), BAD),
+    (dict(T=0.0), BAD), (dict(T=-1.0), BAD), (dict(T=float("nan")), BAD), (dict(T=float("inf")), BAD),
+    (dict(T=1e-5), BAD), (dict(T=1e5), BAD),
+    (dict(k=-1), BAD), (dict(k=101), BAD), (dict(k=129, V=1000, ld=1000), UNSUPPORTED),
+    (dict(logits=None), BAD), (dict(index=None), BAD), (dict(logprob=None), BAD), (dict(entropy=None), BAD),
+    (dict(lse=None), BAD), (dict(top=None), BAD), (dict(ids=None), BAD),
+    (dict(logits=at(0) + 1), BAD), (dict(index=at(1) + 4), BAD), (dict(lse=at(4) + 2), BAD), (dict(ids=at(6) + 4), BAD),
+    (dict(B=0, logits=None), gh.GH_OK),
+])
+def test_token_logprobs_refusals(L, kw, expect):
+    a = dict(logits=at(0), ld=100, index=at(1), B=16, V=100, dtype=gh.GH_BF16, T=1.0, k=5, logprob=at(2),
+             entropy=at(3), lse=at(4), top=at(5), ids=at(6))
+    a.update(kw)
+    assert L.gh_token_logprobs(a["logits"], a["ld"], a["index"], a["B"], a["V"], a["dtype"], -100, a["T"], a["k"],
+                               a["logprob"], a["entropy"], a["lse"], a["top"], a["ids"], None) == expect
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(B=-1), BAD), (dict(V=0), BAD), (dict(ld=99), BAD), (dict(ldg=99), BAD), (dict(dtype=-1), BAD),
+    (dict(T=0.0), BAD), (dict(T=float("nan")), BAD),
+    (dict(logits=None), BAD), (dict(index=None), BAD), (dict(lse=None), BAD), (dict(entropy=None), BAD),
+    (dict(gl=None), BAD), (dict(grad=None), BAD), (dict(grad=at(6) + 1), BAD), (dict(gH=at(5) + 2), BAD),
+    (dict(grad=at(0) + 64), BAD),            # partial overlap
+    (dict(grad=at(0), ldg=128), BAD),        # in place with another row stride
+    (dict(B=0, grad=None), gh.GH_OK),
+])
+def test_token_logprobs_vjp_refusals(L, kw, expect):
+    a = dict(logits=at(0), ld=100, index=at(1), B=16, V=100, dtype=gh.GH_F32, T=1.0, lse=at(2), entropy=at(3),
+             gl=at(4), gH=at(5), grad=at(6), ldg=100)
+    a.update(kw)
+    assert L.gh_token_logprobs_vjp(a["logits"], a["ld"], a["index"], a["B"], a["V"], a["dtype"], -100, a["T"],
+                                   a["lse"], a["entropy"], a["gl"], a["gH"], a["grad"], a["ldg"], None) == expect
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(B=-1), BAD), (dict(V=0), BAD), (dict(K=0), BAD), (dict(K=129), UNSUPPORTED), (dict(ld=99), BAD),
+    (dict(ldg=99), BAD), (dict(dtype=5), BAD), (dict(T=0.0), BAD), (dict(T=float("inf")), BAD), (dict(renorm=2), BAD),
+    (dict(red=3), BAD), (dict(logits=None), BAD), (dict(ids=None), BAD), (dict(vals=None), BAD), (dict(loss=None), BAD),
+    (dict(loss=at(4) + 2), BAD), (dict(total=at(7) + 4), BAD), (dict(row=at(5) + 1), BAD), (dict(vals=at(2) + 2), BAD),
+    (dict(grad=at(0) + 64), BAD), (dict(grad=at(0), ldg=128), BAD),
+])
+def test_topk_distill_refusals(L, kw, expect):
+    a = dict(logits=at(0), ld=100, ids=at(1), vals=at(2), B=16, V=100, K=8, dtype=gh.GH_BF16, T=1.0, renorm=1, red=0,
+             total=None, loss=at(4), row=None, grad=at(6), ldg=100)
+    a.update(kw)
+    assert L.gh_topk_distill(a["logits"], a["ld"], a["ids"], a["vals"], a["B"], a["V"], a["K"], a["dtype"], a["T"],
+                             a["renorm"], a["red"], a["total"], a["loss"], a["row"], a["grad"], a["ldg"],
+                             None) == expect
+
+
+def test_distill_count_refusals(L):
+    assert L.gh_distill_count(at(0), at(1), -1, 8, 100, at(2), None) == BAD
+    assert L.gh_distill_count(at(0), at(1), 4, 0, 100, at(2), None) == BAD
+    assert L.gh_distill_count(at(0), at(1), 4, 129, 100, at(2), None) == UNSUPPORTED
+    assert L.gh_distill_count(at(0), at(1), 4, 8, 100, None, None) == BAD
+    assert L.gh_distill_count(None, at(1), 4, 8, 100, at(2), None) == BAD
+    assert L.gh_distill_count(at(0), at(1), 4, 8, 100, at(2) + 4, None) == BAD
+
+
+def test_python_binding_refuses_cpu_tensors():
+    x, t = torch.zeros(4, 8), torch.zeros(4, dtype=torch.int64)
+    f, ids = torch.zeros(4), torch.zeros(4, 2, dtype=torch.int64)
+    with pytest.raises(ValueError):
+        gh.gh_token_logprobs(x, t)
+    with pytest.raises(ValueError):
+        gh.gh_token_logprobs_vjp(x, t, f, f, f)
+    with pytest.raises(ValueError):
+        gh.gh_topk_distill(x, ids, torch.zeros(4, 2))
+    with pytest.raises(ValueError):
+        gh.gh_distill_count(ids, torch.zeros(4, 2), 8)
