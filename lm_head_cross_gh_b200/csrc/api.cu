@@ -271,6 +271,7 @@ gh_status_t gh_token_logprobs(const void* logits, int64_t ld, const int64_t* ind
   a.V = V;
   a.ld = ld;
   a.ignore_index = ignore_index;
+  a.temperature = temperature;
   a.c = static_cast<float>(1.4426950408889634 / static_cast<double>(temperature));
   a.top_k = static_cast<int>(top_k);
   a.logprob = logprob;

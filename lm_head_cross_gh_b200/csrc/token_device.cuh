@@ -1,0 +1,212 @@
+// Device helpers of the token operators (token_logprobs.cu, topk_distill.cu):
+// row geometry, the (reference, sum, weighted sum) state of a softmax in base 2
+// and its merge, order keys of logits, and a warp's selection of its k largest
+// keys.
+#pragma once
+
+#include <cstdint>
+
+#include "ce_device.cuh"
+#include "common.cuh"
+
+namespace gh {
+namespace {
+
+constexpr float kNaN = __builtin_nanf("");
+constexpr float kPosInf = __builtin_huge_valf();
+
+// A row's bytes in 16-byte chunks, counted from its first byte rounded down to
+// 16: chunks [c_lo, c_hi) lie wholly inside the row; the elements [0, h) and
+// [tail, V), at most 7 (bf16) or 3 (fp32) each, do not fill one.
+struct RowGeo {
+  const uint8_t* src;   // first element
+  const uint8_t* base;  // src rounded down to 16 bytes
+  int lead;             // src - base
+  int64_t c_lo, c_hi;
+  int64_t h, tail;
+};
+
+template <int ES>
+__device__ __forceinline__ RowGeo row_geo(const void* logits, int64_t row, int64_t ld, int64_t V) {
+  RowGeo r;
+  r.src = static_cast<const uint8_t*>(logits) + row * ld * ES;
+  r.lead = static_cast<int>(reinterpret_cast<uintptr_t>(r.src) & 15);
+  r.base = r.src - r.lead;
+  const int64_t span = r.lead + V * ES;
+  r.c_lo = (r.lead + 15) >> 4;
+  r.c_hi = tmax<int64_t>(r.c_lo, span >> 4);
+  r.h = tmin<int64_t>(V, (16 * r.c_lo - r.lead) / ES);
+  r.tail = tmax<int64_t>(r.h, (16 * r.c_hi - r.lead) / ES);
+  return r;
+}
+
+// The ragged-end element of a lane: lanes 0-15 the head, 16-31 the tail; -1: none.
+__device__ __forceinline__ int64_t edge_element(const RowGeo& r, int64_t V, int lane) {
+  if (lane < 16) return lane < r.h ? lane : -1;
+  const int64_t e = r.tail + (lane - 16);
+  return e < V ? e : -1;
+}
+
+// ---- softmax state -------------------------------------------------------------
+// With c = log2(e) / T and y_j = x_j c - R:  s = sum 2^y_j,  t = sum 2^y_j y_j.
+// R is a rounded product; y_j is one fused multiply-add, so R's rounding moves
+// all terms alike and leaves log p_j = ln 2 (y_j - log2 s).  That holds while
+// |R| <= kFarRef (R's rounding is then at most 2^-5); a state with a larger R
+// carries s = 0, and a row whose largest R is one is summed again from
+// differences to its maximum (far_row).  R = +inf marks a NaN or +inf logit.
+constexpr float kFarRef = 1048576.0f;
+
+struct SoftState {
+  float r, s, t;
+};
+
+__device__ __forceinline__ float ref_of(float x, float c) {  // x: not NaN
+  if (x == kPosInf || x == kNegInf) return x;
+  return fminf(fmaxf(x * c, -3e38f), 3e38f);
+}
+
+__device__ __forceinline__ void rescale(SoftState& a, float r) {  // r >= a.r
+  if (a.s != 0.0f) {
+    const float d = a.r - r;
+    const float f = ex2(d);
+    a.t = f * fmaf(a.s, d, a.t);
+    a.s *= f;
+  }
+  a.r = r;
+}
+
+__device__ __forceinline__ SoftState combine(SoftState a, SoftState b) {
+  const float r = fmaxf(a.r, b.r);
+  rescale(a, r);
+  rescale(b, r);
+  return {r, a.s + b.s, a.t + b.t};
+}
+
+__device__ __forceinline__ SoftState warp_combine(SoftState a) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const SoftState b{__shfl_xor_sync(0xffffffffu, a.r, o), __shfl_xor_sync(0xffffffffu, a.s, o),
+                      __shfl_xor_sync(0xffffffffu, a.t, o)};
+    // both lanes of a pair add in the same order
+    const bool low = ((threadIdx.x & 31) & o) == 0;
+    a = low ? combine(a, b) : combine(b, a);
+  }
+  return a;
+}
+
+__device__ __forceinline__ SoftState state_of_element(float x, float c) {
+  if (x != x) return {kPosInf, 0.0f, 0.0f};
+  const float r = ref_of(x, c);
+  if (!(fabsf(r) <= kFarRef)) return {r, 0.0f, 0.0f};
+  const float y = fmaf(x, c, -r), e = ex2(y);
+  return {r, e, e * y};
+}
+
+// A row's distribution: log p = ln 2 ((x - sub) c - r - l2s).
+struct RowDist {
+  float sub, r, l2s, ts;  // ts = t / s
+  bool none;              // no distribution
+};
+
+template <typename T>
+__device__ __forceinline__ float log2_p(const RowDist& d, float x, float c) {
+  return fmaf(x - d.sub, c, -d.r) - d.l2s;
+}
+
+// A row whose logits all lie far from 0 (lowest-value masks, tiny
+// temperatures), by one warp: the maximum, then the sums of (x - max) c.
+template <typename T>
+__device__ __noinline__ RowDist far_row(const uint8_t* src, int64_t V, float c) {
+  constexpr int ES = Elem<T>::kBytes;
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  float m = kNegInf;
+  for (int64_t j = lane; j < V; j += 32) m = fmaxf(m, Elem<T>::load(src + j * ES));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float s = 0.0f, t = 0.0f;
+  for (int64_t j = lane; j < V; j += 32) {
+    const float y = (Elem<T>::load(src + j * ES) - m) * c, e = ex2(y);
+    s += e;
+    if (e > 0.0f) t = fmaf(e, y, t);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    t += __shfl_xor_sync(0xffffffffu, t, o);
+  }
+  return {m, 0.0f, log2f(s), t / s, false};
+}
+
+// The distribution from a row's merged state (the same in every lane).
+template <typename T>
+__device__ __forceinline__ RowDist row_dist(const SoftState& st, const uint8_t* src, int64_t V, float c) {
+  if (st.r == kPosInf || st.r == kNegInf) return {0.0f, 0.0f, 0.0f, 0.0f, true};
+  if (fabsf(st.r) > kFarRef) return far_row<T>(src, V, c);
+  return {0.0f, st.r, log2f(st.s), st.t / st.s, false};
+}
+
+// log-sum-exp of x / temperature (beyond fp32's range infinite, as its rounding is).
+__device__ __forceinline__ float dist_lse(const RowDist& d, float temperature) {
+  return d.sub / temperature + kLn2 * (d.r + d.l2s);
+}
+
+// ---- order keys ------------------------------------------------------------------
+// Order-preserving key of a logit that is not NaN (-0 and +0 alike); 0 is below
+// every logit's key.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t b = __float_as_uint(x + 0.0f);
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+// Key of (value descending, index ascending): the larger comes first.
+__device__ __forceinline__ uint64_t rank_key(uint32_t key, int64_t j) {
+  return (static_cast<uint64_t>(key) << 32) | (0xffffffffu - static_cast<uint32_t>(j));
+}
+__device__ __forceinline__ float key_value(uint64_t key) {
+  const uint32_t k = static_cast<uint32_t>(key >> 32);
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+__device__ __forceinline__ int64_t key_index(uint64_t key) {
+  return static_cast<int64_t>(0xffffffffu - static_cast<uint32_t>(key));
+}
+
+// A warp's k largest of the keys pushed to it (k <= GH_MAX_TOP_K).  Keys at or
+// below `thr` are dropped; when the buffer fills, it is cut to its k largest
+// and `thr` rises to the last of them.  Keys are distinct.
+constexpr int kTopBuf = 256;
+
+struct WarpTopK {
+  uint64_t* buf;  // [kTopBuf], this warp's
+  uint64_t* out;  // [GH_MAX_TOP_K], this warp's
+  int k, n;
+  uint64_t thr;
+
+  __device__ __forceinline__ void push(uint64_t key, bool ok) {
+    const int lane = static_cast<int>(threadIdx.x) & 31;
+    ok = ok && key > thr;
+    const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+    if (mask == 0) return;
+    if (ok) buf[n + __popc(mask & ((1u << lane) - 1))] = key;
+    n += __popc(mask);
+    if (n > kTopBuf - 32) cut();
+  }
+
+  // Leaves the k largest (or all n) in out[], largest first, and in buf[].
+  __device__ __noinline__ void cut() {
+    const int lane = static_cast<int>(threadIdx.x) & 31;
+    __syncwarp();
+    for (int i = lane; i < n; i += 32) {
+      const uint64_t v = buf[i];
+      int above = 0;
+      for (int j = 0; j < n; ++j) above += buf[j] > v ? 1 : 0;
+      if (above < k) out[above] = v;
+    }
+    __syncwarp();
+    n = tmin(n, k);
+    for (int i = lane; i < n; i += 32) buf[i] = out[i];
+    if (n == k) thr = out[k - 1];
+    __syncwarp();
+  }
+};
+
+}  // namespace
+}  // namespace gh

@@ -14,6 +14,7 @@ struct LogprobArgs {
   const int64_t* index;  // [B]
   int64_t B, V, ld;
   int64_t ignore_index;
+  float temperature;
   float c;               // log2(e) / temperature
   int top_k;
   float* logprob;        // [B]
@@ -21,6 +22,23 @@ struct LogprobArgs {
   float* lse;            // [B], of the scaled logits
   float* top_logprob;    // [B, top_k]
   int64_t* top_index;    // [B, top_k]
+};
+
+// Row sums over units (a row, or one of `slices` slices of it): straight to the
+// log-probability outputs (part null), or as partial states to merge.
+struct StatArgs {
+  const void* logits;
+  int64_t B, V, ld;
+  float c;             // log2(e) / temperature
+  uint32_t low;        // lowest logit whose x c is finite (packed bf16, or fp32 bits)
+  int slices;          // per row
+  int slice_segs;      // 128-byte segments per slice
+  int seg_cap;         // keys kept per unit, a multiple of 128
+  int top_k;
+  const int8_t* flags; // [B] 1: the row counts (null: by lp.index)
+  float4* part;        // [B * slices] (reference, sum, weighted sum, -)
+  uint64_t* part_keys; // [B * slices, top_k], 0: none
+  LogprobArgs lp;
 };
 
 struct LogprobVjpArgs {
