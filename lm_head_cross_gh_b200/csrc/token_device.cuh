@@ -66,12 +66,11 @@ __device__ __forceinline__ float ref_of(float x, float c) {  // x: not NaN
 }
 
 __device__ __forceinline__ void rescale(SoftState& a, float r) {  // r >= a.r
-  if (a.s != 0.0f) {
-    const float d = a.r - r;
-    const float f = ex2(d);
-    a.t = f * fmaf(a.s, d, a.t);
-    a.s *= f;
-  }
+  // a sum of 0 (its a.r may be infinite) stays 0; others have a finite distance
+  const float d = a.s == 0.0f ? 0.0f : a.r - r;
+  const float f = ex2(d);
+  a.t = f * fmaf(a.s, d, a.t);
+  a.s *= f;
   a.r = r;
 }
 

@@ -197,6 +197,20 @@ __device__ __forceinline__ Unit unit_of(const StatArgs& a, int64_t u, int64_t ro
   return w;
 }
 
+// A unit's chunk count alone (what the consumers need of it).
+template <int ES>
+__device__ __forceinline__ int unit_chunks(const StatArgs& a, int64_t u) {
+  const int64_t row = unit_row(a, u);
+  const uint32_t lead = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(a.logits) + static_cast<uintptr_t>(row * a.ld) * ES) & 15u;
+  const int lo = static_cast<int>((lead + 15) >> 4);
+  const int n = tmax(0, static_cast<int>((lead + a.V * ES) >> 4) - lo);
+  if (a.slices == 1) return n;
+  const int slice = static_cast<int>(u - row * a.slices), per = a.slice_segs * kSegChunks;
+  const int64_t from = static_cast<int64_t>(slice) * per;
+  const int left = static_cast<int>(tmax<int64_t>(0, n - from));
+  return slice == a.slices - 1 ? left : tmin(left, per);
+}
+
 // Rows that count: 1; ignored: 0; an index outside [0, V): -1.
 __device__ __forceinline__ int row_kind(const StatArgs& a, int64_t row) {
   if (a.flags) return a.flags[row];
@@ -415,13 +429,16 @@ __global__ void __launch_bounds__(kLpThreads, 1) logprobs_ring_kernel(StatArgs a
       // this lane's 16 thread states, largest reference first
       SoftState st = state_of_element(edge, a.c);
       float m = st.r;
+      float2 rs[kLpWarps];
 #pragma unroll
-      for (int v = 0; v < kLpWarps; ++v) m = fmaxf(m, sh.part_rs[f][v][lane].x);
+      for (int v = 0; v < kLpWarps; ++v) {
+        rs[v] = sh.part_rs[f][v][lane];
+        m = fmaxf(m, rs[v].x);
+      }
       rescale(st, m);
 #pragma unroll
       for (int v = 0; v < kLpWarps; ++v) {
-        const float2 rs = sh.part_rs[f][v][lane];
-        SoftState o{rs.x, rs.y, ENT ? sh.part_t[f][v][lane] : 0.0f};
+        SoftState o{rs[v].x, rs[v].y, ENT ? sh.part_t[f][v][lane] : 0.0f};
         rescale(o, m);
         st.s += o.s;
         st.t += o.t;
@@ -464,7 +481,15 @@ __global__ void __launch_bounds__(kLpThreads, 1) logprobs_ring_kernel(StatArgs a
   // ---------------- consumers ----------------
   const int grp = warp / kLpGroupWarps;
   const int gtid = static_cast<int>(threadIdx.x) - grp * kLpGroupThreads;
-  uint32_t n = 0, k = 0;  // pieces, units that count
+  constexpr uint32_t kGroupSlots = kSlots / kLpGroups;  // a group's slots: grp, grp + 4, ...
+  static_assert(kSlots % kLpGroups == 0, "a slot always serves the same group");
+  uint32_t turn = static_cast<uint32_t>(grp);  // pieces of this unit before the group's next one
+  uint32_t gs = 0, gphase = 0;                 // the group's next slot and its phase
+  uint32_t j = 0, jphase = 1;                  // the unit's state buffer and its phase
+  // chunk i ^ (gtid % 8) of the thread's segment: eight threads' loads of 16
+  // bytes then fall into different banks
+  const uint32_t swz = static_cast<uint32_t>(gtid & 7);
+  const uint8_t* const my_seg = ring + grp * kLpPieceBytes + 128 * gtid + 16 * swz;
   int kind = kind_of(first);
   for (int64_t u = first; u < units; u += G) {
     const int next = kind_of(u + G);
@@ -473,49 +498,52 @@ __global__ void __launch_bounds__(kLpThreads, 1) logprobs_ring_kernel(StatArgs a
       continue;
     }
     kind = next;
-    const int64_t row = unit_row(a, u);
-    const RowGeo r = row_geo<ES>(a.logits, row, a.ld, a.V);
-    const Unit w = unit_of(a, u, row, r);
-    const int nc_all = static_cast<int>(w.c1 - w.c0);
-    const int j = static_cast<int>(k % kLpFinalizers);
+    const int nc_all = unit_chunks<ES>(a, u);
+    const uint32_t np = static_cast<uint32_t>(nc_all + kLpPieceChunks - 1) / kLpPieceChunks;
     // the unit's states and keys go where unit k - 4's were
     bool ok = true;
-    if (lane == 0) ok = wait(&sh.rowempty[j], ((k / kLpFinalizers) & 1) ^ 1);
+    if (lane == 0) ok = wait(&sh.rowempty[j], jphase);
     if (!__all_sync(0xffffffffu, ok)) break;
     SoftState st{kNegInf, 0.0f, 0.0f};
-    for (int c0 = 0; c0 < nc_all; c0 += kLpPieceChunks, ++n) {
-      if (static_cast<int>(n % kLpGroups) != grp) continue;
-      const uint32_t s = n % kSlots;
-      if (!__all_sync(0xffffffffu, wait(&sh.full[s], (n / kSlots) & 1))) {
+    for (; turn < np; turn += kLpGroups) {
+      const uint32_t s = gs * kLpGroups + grp;
+      if (!__all_sync(0xffffffffu, wait(&sh.full[s], gphase))) {
         ok = false;
         break;
       }
-      // chunk i ^ (gtid % 8) of the thread's segment: eight threads' loads of 16
-      // bytes then fall into different banks
-      const uint8_t* seg = ring + s * kLpPieceBytes + 128 * gtid;
-      const int nc = tmin(kSegChunks, nc_all - c0 - kSegChunks * gtid);
+      const uint8_t* seg = my_seg + gs * (kLpGroups * kLpPieceBytes);
+      if (++gs == kGroupSlots) {
+        gs = 0;
+        gphase ^= 1;
+      }
+      const int nc = nc_all - static_cast<int>(turn) * kLpPieceChunks - kSegChunks * gtid;
       uint4 q[kSegChunks];
 #pragma unroll
-      for (int i = 0; i < kSegChunks; ++i) q[i] = *reinterpret_cast<const uint4*>(seg + 16 * (i ^ (gtid & 7)));
+      for (int i = 0; i < kSegChunks; ++i)
+        q[i] = *reinterpret_cast<const uint4*>(seg + (static_cast<int>((i ^ swz)) - static_cast<int>(swz)) * 16);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.empty[s]);
       if (nc < kSegChunks) {  // a row's last piece: no chunks there
         const uint32_t none = ES == 2 ? 0xff80ff80u : 0xff800000u;
 #pragma unroll
         for (int i = 0; i < kSegChunks; ++i)
-          if ((i ^ (gtid & 7)) >= nc) q[i] = make_uint4(none, none, none, none);
+          if (static_cast<int>(i ^ swz) >= nc) q[i] = make_uint4(none, none, none, none);
       }
       if (nc > 0) {
         const float cm = fold_segment<T, ENT>(st, q, a.c, a.low);
-        if constexpr (TOPK) seg_keys[j * a.seg_cap + c0 / kSegChunks + gtid] = order_key(cm);
+        if constexpr (TOPK) seg_keys[j * a.seg_cap + turn * kPieceSegs + gtid] = order_key(cm);
       }
     }
     if (!ok) break;
+    turn -= np;
     sh.part_rs[j][warp][lane] = make_float2(st.r, st.s);
     if constexpr (ENT) sh.part_t[j][warp][lane] = st.t;
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.rowfull[j]);
-    ++k;
+    if (++j == kLpFinalizers) {
+      j = 0;
+      jphase ^= 1;
+    }
   }
 }
 
