@@ -285,7 +285,7 @@ gh_status_t gh_selective_log_softmax(const void* logits, const int64_t* index, i
  *            apart (ld >= V), so a head padded to a round size is read in place.
  *   index    [B] int64, device: the given tokens.
  *   B >= 0, V >= 1 (V < 2^31).
- *   ignore_index  rows with this index are not read: logprob, entropy and lse
+ *   ignore_index  rows with this index do not count: logprob, entropy and lse
  *            are 0, the alternatives -inf with index -1.
  *   temperature   in [1e-4, 1e4].
  *   top_k    0 <= top_k <= V, at most GH_MAX_TOP_K.

@@ -190,7 +190,13 @@ struct WarpTopK {
   }
 
   // Leaves the k largest (or all n) in out[], largest first, and in buf[].
-  __device__ __noinline__ void cut() {
+  __device__ __forceinline__ void cut() {
+    cut_keys(buf, out, n, k);
+    n = tmin(n, k);
+    if (n == k) thr = out[k - 1];
+  }
+
+  static __device__ __noinline__ void cut_keys(uint64_t* buf, uint64_t* out, int n, int k) {
     const int lane = static_cast<int>(threadIdx.x) & 31;
     __syncwarp();
     for (int i = lane; i < n; i += 32) {
@@ -200,9 +206,7 @@ struct WarpTopK {
       if (above < k) out[above] = v;
     }
     __syncwarp();
-    n = tmin(n, k);
-    for (int i = lane; i < n; i += 32) buf[i] = out[i];
-    if (n == k) thr = out[k - 1];
+    for (int i = lane; i < tmin(n, k); i += 32) buf[i] = out[i];
     __syncwarp();
   }
 };

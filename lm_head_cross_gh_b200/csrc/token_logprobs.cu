@@ -10,13 +10,13 @@
 // The alternatives are the top_k logits by (value descending, index
 // ascending); the temperature does not change their order.
 //
-// The forward (logprobs_ring_kernel) reads every logit once.  A row is cut
-// into segments of 128 bytes; the thread that sums a segment also has its
-// largest logit, whose key it keeps in shared memory.  The k largest logits lie
-// in the k segments that come first by (largest logit descending, position
-// ascending): any other segment's logits have k segment maxima before them.
-// So the alternatives cost one key per segment during the pass, a selection
-// among V / 64 (bf16) keys by one warp, and k segments read again from L2.
+// The forward (logprobs_kernel) reads every logit once.  A row is cut into
+// segments of 512 bytes, one 16-byte load of a warp each; the warp that sums a
+// segment keeps the key of its largest logit in shared memory.  The k largest
+// logits lie in the k segments that come first by (largest logit descending,
+// position ascending): any other segment's logits have k segment maxima before
+// them.  So the alternatives cost one warp maximum per segment during the
+// pass, a selection among V / 256 (bf16) keys, and k segments read again from L2.
 #include <algorithm>
 #include <cstring>
 
@@ -30,52 +30,40 @@ namespace gh {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Forward: one persistent CTA per SM streams units (a row, or a slice of one)
-// through a ring of 16 KiB pieces, as the cross-entropy ring does:
-//   warp 16      producer: bulk copies into the next free slot
-//   warps 0-15   consumers, four groups of four warps; piece n goes to group
-//                n % 4, a thread takes one segment (8 chunks) into registers,
-//                frees the slot and folds the segment into its state
-//   warps 17-20  finalizers, unit k to warp 17 + k % 4: merge the 512 thread
-//                states with the ragged ends, pick the alternatives, write
+// Forward.  One CTA of four warps per unit (a row, or a slice of one), seven or
+// eight of them on an SM, so that one's end (merge, alternatives) overlaps the
+// others' streams.  The warps take batches of four segments in turn, the next
+// batch's loads in flight while one is summed.
+//
+// Bound by HBM for fp32 logits ([4096, 50257]: 128 us, 6.4 TB/s), by the
+// exponentials and the instructions around them for bf16 ([8192, 50257]: 150
+// us).  Measured beside it on that shape: a ring of bulk copies with consumer
+// and finalizer warps 162 us (its row ends keep one warp busy for longer than a
+// row lasts: 328 us with 20 alternatives, 196 here), two warps per CTA 152 us,
+// eight 166 us, CTAs that take over the next row through launch control 172 us
+// (it spills).
 // ---------------------------------------------------------------------------
 
-constexpr int kLpWarps = 16;
-constexpr int kLpGroups = 4;
-constexpr int kLpGroupWarps = kLpWarps / kLpGroups;
-constexpr int kLpGroupThreads = 32 * kLpGroupWarps;
-constexpr int kLpFinalizers = 4;
-constexpr int kLpThreads = 32 * (kLpWarps + 1 + kLpFinalizers);
-constexpr int kLpPieceBytes = 16384;
-constexpr int kLpPieceChunks = kLpPieceBytes / 16;
-constexpr int kSegChunks = 8;  // 128 bytes
-constexpr int kPieceSegs = kLpPieceChunks / kSegChunks;
-static_assert(kPieceSegs == kLpGroupThreads, "one segment per thread of a group");
-// Ring slots: with alternatives part of shared memory holds the segments' keys.
-template <bool TOPK>
-constexpr int kLpSlots = TOPK ? 8 : 12;
-constexpr int kLpMaxSegs = 3584;  // segments of a unit whose keys fit beside 8 slots
+constexpr int kLpWarps = 4;
+constexpr int kLpThreads = 32 * kLpWarps;
+constexpr int kBatch = 4;
+constexpr int kSegChunks = 32;  // 512 bytes
+constexpr int kBatchChunks = kBatch * kSegChunks;
+constexpr int kLpMaxSegs = 2048;  // segments of a unit whose keys are kept (8 KiB)
+constexpr int kCandidates = 512;  // logits of the picked segments that reach the threshold, before the slow way
 
 struct LpShared {
-  uint64_t full[12], empty[12];
-  uint64_t rowfull[kLpFinalizers], rowempty[kLpFinalizers];
-  float2 part_rs[kLpFinalizers][kLpWarps][32];
-  float part_t[kLpFinalizers][kLpWarps][32];
-  int abort;
+  float4 state[kLpWarps];  // the warps' (reference, sum, weighted sum)
+  RowDist dist;
+  int count, listed;
+  float least;
+  int list[GH_MAX_TOP_K];
 };
 struct LpTopShared {
-  uint64_t buf[kLpFinalizers][kTopBuf];
-  uint64_t out[kLpFinalizers][GH_MAX_TOP_K];
-  int list[kLpFinalizers][GH_MAX_TOP_K];
+  uint64_t buf[kCandidates];
+  uint64_t out[GH_MAX_TOP_K];
 };
-constexpr int kLpHdrBytes = (static_cast<int>(sizeof(LpShared)) + 127) / 128 * 128;
-constexpr int kLpTopBytes = (static_cast<int>(sizeof(LpTopShared)) + 127) / 128 * 128;
-
-template <bool TOPK>
-constexpr int lp_smem_bytes(int segs) {
-  return kLpHdrBytes + kLpSlots<TOPK> * kLpPieceBytes + (TOPK ? kLpTopBytes + kLpFinalizers * 4 * segs : 0);
-}
-static_assert(lp_smem_bytes<true>(kLpMaxSegs) <= 227 * 1024 && lp_smem_bytes<false>(0) <= 227 * 1024, "");
+static_assert(kCandidates >= kTopBuf, "the slow way's buffer");
 
 __device__ __forceinline__ uint32_t bf16x2_max_nan(uint32_t a, uint32_t b) {
   uint32_t d;
@@ -131,51 +119,69 @@ __device__ __forceinline__ uint4 clamp_low<float>(const uint4& q, uint32_t low) 
                     __float_as_uint(fmaxf(__uint_as_float(q.z), l)), __float_as_uint(fmaxf(__uint_as_float(q.w), l)));
 }
 
-// Folds a segment (N chunks in registers) into a thread's state; returns its
-// largest logit.
-template <typename T, bool ENT, int N>
-__device__ __forceinline__ float fold_segment(SoftState& st, const uint4 (&q)[N], float c, uint32_t low) {
-  constexpr int EPC = 16 / Elem<T>::kBytes;
-  uint4 m4 = q[0];
+// Largest of the warp's values; NaN if there is one.
+__device__ __forceinline__ float warp_max_nan(float v) {
+  float d;
+  asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(v));
+  return d;
+}
+
+// A warp's running sums: one reference for its lanes (the largest logit so
+// far), so it rises seldom and the lanes' sums add without rescaling.
+struct WarpSums {
+  float m;         // largest logit so far (-inf: none; +inf: a NaN or +inf was seen)
+  float r;         // its reference, ref_of(m)
+  float2 s[2], t[2];
+};
+
+// A batch's largest logit is `m` (NaN if it has one): raise the reference.
+__device__ __forceinline__ void raise(WarpSums& w, float m, float c) {
+  const float top = m < kPosInf ? m : kPosInf;
+  const float r = ref_of(top, c);
+  const bool sums = fabsf(w.r) <= kFarRef;  // else there is nothing to rescale yet
+  const float d = sums ? fmaxf(w.r - r, -2.0f * kFarRef) : 0.0f, f = ex2(d);
 #pragma unroll
-  for (int i = 1; i < N; ++i) m4 = max4<T>(m4, q[i]);
-  const float cm = max_of4<T>(m4);
-  if (!(cm < kPosInf)) {
-    st = {kPosInf, 0.0f, 0.0f};
-    return cm;
+  for (int i = 0; i < 2; ++i) {
+    w.t[i] = make_float2(f * fmaf(w.s[i].x, d, w.t[i].x), f * fmaf(w.s[i].y, d, w.t[i].y));
+    w.s[i] = make_float2(f * w.s[i].x, f * w.s[i].y);
   }
-  const float r = ref_of(cm, c);
-  if (r > st.r) rescale(st, r);
-  if (!(r >= -kFarRef && st.r <= kFarRef)) return cm;
-  const float2 c2 = make_float2(c, c), nr = make_float2(-st.r, -st.r);
-  float2 s[4], t[2];
+  w.m = top;
+  w.r = r;
+}
+
+// Folds a lane's chunks of a batch into its warp's sums.  TOPK: the segments'
+// largest logits go to m[].
+template <typename T, bool ENT, bool TOPK>
+__device__ __forceinline__ void fold_batch(WarpSums& w, const uint4 (&q)[kBatch], float c, uint32_t low,
+                                           float (&m)[kBatch]) {
+  constexpr int EPC = 16 / Elem<T>::kBytes;
+  float bm;
+  if constexpr (TOPK) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) s[i] = make_float2(0.0f, 0.0f);
+    for (int i = 0; i < kBatch; ++i) m[i] = warp_max_nan(max_of4<T>(q[i]));
+    bm = f32_max_nan(f32_max_nan(m[0], m[1]), f32_max_nan(m[2], m[3]));
+  } else {
+    bm = warp_max_nan(max_of4<T>(max4<T>(max4<T>(q[0], q[1]), max4<T>(q[2], q[3]))));
+  }
+  if (!(bm <= w.m)) raise(w, bm, c);
+  if (!(fabsf(w.r) <= kFarRef)) return;
+  const float2 c2 = make_float2(c, c), nr = make_float2(-w.r, -w.r);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) t[i] = make_float2(0.0f, 0.0f);
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
+  for (int i = 0; i < kBatch; ++i) {
     float v[EPC];
     unpack16<T>(ENT ? clamp_low<T>(q[i], low) : q[i], v);
 #pragma unroll
     for (int j = 0; j < EPC; j += 2) {
       const float2 y = __ffma2_rn(make_float2(v[j], v[j + 1]), c2, nr);
       const float2 e = make_float2(ex2(y.x), ex2(y.y));
-      float2& a = s[(i * EPC / 2 + j / 2) & 3];
+      float2& a = w.s[(j / 2) & 1];
       a = __fadd2_rn(a, e);
       if constexpr (ENT) {
-        float2& b = t[(j / 2) & 1];
+        float2& b = w.t[(j / 2) & 1];
         b = __ffma2_rn(e, y, b);
       }
     }
   }
-  const float2 sa = __fadd2_rn(__fadd2_rn(s[0], s[1]), __fadd2_rn(s[2], s[3]));
-  st.s += sa.x + sa.y;
-  if constexpr (ENT) {
-    const float2 tb = __fadd2_rn(t[0], t[1]);
-    st.t += tb.x + tb.y;
-  }
-  return cm;
 }
 
 // Where unit u lies: row, slice, and its chunks of the row.
@@ -195,20 +201,6 @@ __device__ __forceinline__ Unit unit_of(const StatArgs& a, int64_t u, int64_t ro
   w.c0 = tmin(r.c_hi, r.c_lo + w.slice * per);
   w.c1 = w.slice == a.slices - 1 ? r.c_hi : tmin(r.c_hi, w.c0 + per);
   return w;
-}
-
-// A unit's chunk count alone (what the consumers need of it).
-template <int ES>
-__device__ __forceinline__ int unit_chunks(const StatArgs& a, int64_t u) {
-  const int64_t row = unit_row(a, u);
-  const uint32_t lead = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(a.logits) + static_cast<uintptr_t>(row * a.ld) * ES) & 15u;
-  const int lo = static_cast<int>((lead + 15) >> 4);
-  const int n = tmax(0, static_cast<int>((lead + a.V * ES) >> 4) - lo);
-  if (a.slices == 1) return n;
-  const int slice = static_cast<int>(u - row * a.slices), per = a.slice_segs * kSegChunks;
-  const int64_t from = static_cast<int64_t>(slice) * per;
-  const int left = static_cast<int>(tmax<int64_t>(0, n - from));
-  return slice == a.slices - 1 ? left : tmin(left, per);
 }
 
 // Rows that count: 1; ignored: 0; an index outside [0, V): -1.
@@ -233,316 +225,316 @@ __device__ __forceinline__ void write_no_row(const LogprobArgs& o, int64_t row, 
   }
 }
 
-// Outputs of a row that counts, from its distribution and its alternatives'
-// keys, largest first (by one warp).
+// One alternative of a row.
 template <typename T>
-__device__ __forceinline__ void write_row(const LogprobArgs& o, int64_t row, const RowDist& d, float xt,
-                                          const uint64_t* top) {
+__device__ __forceinline__ void write_top(const LogprobArgs& o, int64_t row, const RowDist& d, int k, uint64_t key) {
+  o.top_logprob[row * o.top_k + k] = d.none ? kNaN : kLn2 * log2_p<T>(d, key_value(key), o.c);
+  o.top_index[row * o.top_k + k] = d.none ? -1 : key_index(key);
+}
+
+// Values of a row that counts (by one thread).
+template <typename T>
+__device__ __forceinline__ void write_values(const LogprobArgs& o, int64_t row, const RowDist& d, float xt) {
+  o.logprob[row] = d.none ? kNaN : kLn2 * log2_p<T>(d, xt, o.c);
+  o.entropy[row] = d.none ? kNaN : kLn2 * (d.l2s - d.ts);
+  o.lse[row] = d.none ? kNaN : dist_lse(d, o.temperature);
+}
+
+// The k-th largest of keys[] (n4 groups of four, zeros as padding), found bit by
+// bit, by one warp; stops at a prefix that exactly k keys reach (*exact).  bf16
+// keys differ in their upper 16 bits only.  R > 0: up to 32 R groups, kept in
+// registers.
+template <typename T, int R>
+__device__ __forceinline__ uint32_t kth_key(const uint32_t* keys, int n4, int k, bool* exact) {
   const int lane = static_cast<int>(threadIdx.x) & 31;
-  if (lane == 0) {
-    o.logprob[row] = d.none ? kNaN : kLn2 * log2_p<T>(d, xt, o.c);
-    o.entropy[row] = d.none ? kNaN : kLn2 * (d.l2s - d.ts);
-    o.lse[row] = d.none ? kNaN : dist_lse(d, o.temperature);
+  const uint4* k4 = reinterpret_cast<const uint4*>(keys);
+  uint4 v[R > 0 ? R : 1];
+  if constexpr (R > 0) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) v[i] = 32 * i + lane < n4 ? k4[32 * i + lane] : make_uint4(0, 0, 0, 0);
   }
-  for (int k = lane; k < o.top_k; k += 32) {
-    o.top_logprob[row * o.top_k + k] = d.none ? kNaN : kLn2 * log2_p<T>(d, key_value(top[k]), o.c);
-    o.top_index[row * o.top_k + k] = d.none ? -1 : key_index(top[k]);
+  auto reach = [](const uint4& q, uint32_t c) { return (q.x >= c) + (q.y >= c) + (q.z >= c) + (q.w >= c); };
+  constexpr int kLastBit = Elem<T>::kBytes == 2 ? 16 : 0;
+  uint32_t key = 0;
+  *exact = false;
+  for (int bit = 31; bit >= kLastBit; --bit) {
+    const uint32_t cand = key | (1u << bit);
+    int n = 0;
+    if constexpr (R > 0) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) n += reach(v[i], cand);
+    } else {
+      for (int i = lane; i < n4; i += 32) n += reach(k4[i], cand);
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (n >= k) key = cand;
+    if (n == k) {
+      *exact = true;
+      break;
+    }
   }
+  return key;
 }
 
 // The first k segments by (key descending, position ascending) of `segs` keys
-// (padded with zeros to a multiple of 128): their positions into list[],
-// returns how many and, in thr, a key that k of all the logits reach (0 where
-// fewer segments than k exist).  The k-th largest key is found bit by bit,
-// stopping as soon as a prefix has exactly k keys at or above it; bf16 keys
-// differ in their upper 16 bits only.
+// (padded with zeros to a multiple of 128), by one warp: their positions into
+// list[], in no order unless keys tie; returns how many, and in thr a key that
+// k of all the logits reach (0 where there are no more than k segments).
 template <typename T>
 __device__ __forceinline__ int pick_segments(const uint32_t* keys, int segs, int k, int* list, uint32_t* thr) {
   const int lane = static_cast<int>(threadIdx.x) & 31;
   if (segs <= k) {
     for (int i = lane; i < segs; i += 32) list[i] = i;
     *thr = 0;
-    __syncwarp();
     return segs;
   }
-  const uint4* k4 = reinterpret_cast<const uint4*>(keys);
-  const int n4 = (segs + 127) / 128 * 32;
-  uint32_t key = 0;
-  constexpr int kLastBit = Elem<T>::kBytes == 2 ? 16 : 0;
-  for (int bit = 31; bit >= kLastBit; --bit) {
-    const uint32_t cand = key | (1u << bit);
-    int n = 0;
-    for (int i = lane; i < n4; i += 32) {
-      const uint4 v = k4[i];
-      n += (v.x >= cand) + (v.y >= cand) + (v.z >= cand) + (v.w >= cand);
-    }
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (n >= k) key = cand;
-    if (n == k) break;
-  }
-  // For bf16 a negative value's key ends in ones; compare on the kept bits.
-  const uint32_t mask = kLastBit ? 0xffff0000u : 0xffffffffu;
-  int above = 0;
-  for (int i = lane; i < n4; i += 32) {
-    const uint4 v = k4[i];
-    above += ((v.x & mask) > key) + ((v.y & mask) > key) + ((v.z & mask) > key) + ((v.w & mask) > key);
-  }
-  int left = k - __reduce_add_sync(0xffffffffu, above);  // how many of the equal ones, in order
-  int n = 0;
+  bool exact;
+  const int n4 = (segs + 3) / 4;
+  const uint32_t key = n4 <= 64 ? kth_key<T, 2>(keys, n4, k, &exact) : kth_key<T, 0>(keys, n4, k, &exact);
+  *thr = key;
   const uint32_t below = (1u << lane) - 1;
+  int n = 0;
+  if (exact) {
+    for (int i = 0; i < segs; i += 32) {
+      const bool take = i + lane < segs && keys[i + lane] >= key;
+      const uint32_t got = __ballot_sync(0xffffffffu, take);
+      if (take) list[n + __popc(got & below)] = i + lane;
+      n += __popc(got);
+    }
+    return n;
+  }
+  // Some keys tie at the k-th: all above it, and the first of the equal ones.
+  // (A negative bf16 value's key ends in ones: compare the kept bits.)
+  const uint32_t mask = Elem<T>::kBytes == 2 ? 0xffff0000u : 0xffffffffu;
+  int above = 0;
+  for (int i = lane; i < segs; i += 32) above += (keys[i] & mask) > key;
+  int left = k - __reduce_add_sync(0xffffffffu, above);
   for (int i = 0; i < segs && n < k; i += 32) {
     const uint32_t v = i + lane < segs ? keys[i + lane] & mask : 0u;
-    const uint32_t eq = __ballot_sync(0xffffffffu, v == key && i + lane < segs);
-    const bool take = v > key || (v == key && i + lane < segs && __popc(eq & below) < left);
+    const uint32_t eq = __ballot_sync(0xffffffffu, v == key);
+    const bool take = v > key || (v == key && __popc(eq & below) < left);
     const uint32_t got = __ballot_sync(0xffffffffu, take);
     if (take) list[n + __popc(got & below)] = i + lane;
     n += __popc(got);
     left -= tmin(left, __popc(eq));
   }
-  *thr = key;
-  __syncwarp();
   return n;
 }
 
-// Pushes the logits of the listed segments of a unit (chunks from c0 on).
+// A threshold key as a logit: keys at or above it are logits >= it.
 template <typename T>
-__device__ __forceinline__ void push_segments(WarpTopK& top, const RowGeo& r, const Unit& w, const int* list, int n) {
+__device__ __forceinline__ float least_of(uint32_t thr) {
+  if (thr == 0) return kNegInf;
+  if (Elem<T>::kBytes == 2 && !(thr & 0x80000000u)) thr |= 0xffffu;  // the bf16 value itself
+  return key_value(static_cast<uint64_t>(thr) << 32);
+}
+
+// Which elements of a chunk are >= least (bit j: element j).
+template <typename T>
+__device__ __forceinline__ uint32_t reach_mask(const uint4& q, float least) {
+  constexpr int EPC = 16 / Elem<T>::kBytes;
+  float v[EPC];
+  unpack16<T>(q, v);
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < EPC; ++j) m |= (v[j] >= least ? 1u : 0u) << j;
+  return m;
+}
+
+// The k largest keys of the listed segments and the ragged ends, by one warp
+// and whatever their number (ties can make it large): out[] and the count.
+template <typename T>
+__device__ __noinline__ int pick_slowly(LpTopShared& tsh, const RowGeo& r, const Unit& w, const int* list, int n, int k,
+                                        float edge, int64_t e) {
   constexpr int ES = Elem<T>::kBytes, EPC = 16 / ES;
   const int lane = static_cast<int>(threadIdx.x) & 31;
-  auto chunk_of = [&](int i) -> int64_t {
-    const int j = i + (lane >> 3);
-    return j < n ? w.c0 + static_cast<int64_t>(list[j]) * kSegChunks + (lane & 7) : w.c1;
-  };
-  auto load = [&](int64_t c) {
-    return c < w.c1 ? __ldcg(reinterpret_cast<const uint4*>(r.base + 16 * c)) : make_uint4(0, 0, 0, 0);
-  };
-  int64_t c = chunk_of(0);
-  uint4 q = load(c);
-  for (int i = 0; i < n; i += 4) {
-    const int64_t cn = chunk_of(i + 4);
-    const uint4 qn = load(cn);
+  WarpTopK top{tsh.buf, tsh.out, k, 0, 0};
+  for (int i = 0; i < n; ++i) {
+    const int64_t c = w.c0 + static_cast<int64_t>(list[i]) * kSegChunks + lane;
+    const uint4 q = c < w.c1 ? __ldcg(reinterpret_cast<const uint4*>(r.base + 16 * c)) : make_uint4(0, 0, 0, 0);
     float v[EPC];
     unpack16<T>(q, v);
     const int64_t j0 = (16 * c - r.lead) / ES;
 #pragma unroll
-    for (int e = 0; e < EPC; ++e) top.push(rank_key(order_key(v[e]), j0 + e), c < w.c1);
-    c = cn;
-    q = qn;
+    for (int j = 0; j < EPC; ++j) top.push(rank_key(order_key(v[j]), j0 + j), c < w.c1);
   }
+  top.push(rank_key(order_key(edge), e), e >= 0);
+  top.cut();
+  return top.n;
 }
 
 template <typename T, bool ENT, bool TOPK>
-__global__ void __launch_bounds__(kLpThreads, 1) logprobs_ring_kernel(StatArgs a) {
-  constexpr int ES = Elem<T>::kBytes;
-  constexpr uint32_t kSlots = kLpSlots<TOPK>;
-  extern __shared__ __align__(128) uint8_t smem[];
-  LpShared& sh = *reinterpret_cast<LpShared*>(smem);
-  uint8_t* ring = smem + kLpHdrBytes;
-  LpTopShared& tsh = *reinterpret_cast<LpTopShared*>(ring + kSlots * kLpPieceBytes);
-  uint32_t* seg_keys = reinterpret_cast<uint32_t*>(ring + kSlots * kLpPieceBytes + kLpTopBytes);
+__global__ void __launch_bounds__(kLpThreads, TOPK ? 7 : 8) logprobs_kernel(StatArgs a) {
+  constexpr int ES = Elem<T>::kBytes, EPC = 16 / ES;
+  __shared__ LpShared sh;
+  __shared__ LpTopShared tsh;
+  extern __shared__ __align__(16) uint32_t seg_keys[];
   const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
-  const int64_t G = gridDim.x, first = blockIdx.x, units = a.B * a.slices;
-
-  if (threadIdx.x == 0) {
-    for (uint32_t i = 0; i < kSlots; ++i) {
-      mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], kLpGroupWarps);
-    }
-    for (int i = 0; i < kLpFinalizers; ++i) {
-      mbar_init(&sh.rowfull[i], kLpWarps);
-      mbar_init(&sh.rowempty[i], 1);
-    }
-    sh.abort = 0;
-    fence_mbar_init();
-  }
+  const int tid = static_cast<int>(threadIdx.x);
   pdl_wait();
   pdl_trigger();
-  __syncthreads();
-
-  volatile int* abort_flag = &sh.abort;
-  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (*abort_flag) return false;
-    if (mbar_wait(bar, parity)) return true;
-    *abort_flag = 1;
-    return false;
+  const int64_t u = blockIdx.x;
+  const int64_t row = unit_row(a, u);
+  const RowGeo r = row_geo<ES>(a.logits, row, a.ld, a.V);
+  const Unit w = unit_of(a, u, row, r);
+  const int nc = static_cast<int>(w.c1 - w.c0);
+  const uint4* const chunks = reinterpret_cast<const uint4*>(r.base) + w.c0 + lane;
+  const uint32_t none = ES == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
+  auto load = [&](uint4 (&q)[kBatch], int c0) {  // c0: the batch's first chunk of the unit
+    if (c0 + kBatchChunks <= nc) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) q[i] = __ldcg(chunks + c0 + i * kSegChunks);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        q[i] = make_uint4(none, none, none, none);
+        if (c0 + i * kSegChunks + lane < nc) q[i] = __ldcg(chunks + c0 + i * kSegChunks);
+      }
+    }
   };
-  auto kind_of = [&](int64_t u) -> int { return u < units ? row_kind(a, unit_row(a, u)) : 0; };
-
-  if (warp == kLpWarps) {
-    // ---------------- producer ----------------
-    if (lane == 0) {
-      uint32_t n = 0;  // pieces issued
-      int kind = kind_of(first);
-      for (int64_t u = first; u < units; u += G) {
-        const int next = kind_of(u + G);
-        if (kind > 0) {
-          const int64_t row = unit_row(a, u);
-          const RowGeo r = row_geo<ES>(a.logits, row, a.ld, a.V);
-          const Unit w = unit_of(a, u, row, r);
-          for (int64_t c0 = w.c0; c0 < w.c1; c0 += kLpPieceChunks, ++n) {
-            const uint32_t s = n % kSlots;
-            if (!wait(&sh.empty[s], ((n / kSlots) & 1) ^ 1)) break;
-            const uint32_t bytes = 16u * static_cast<uint32_t>(tmin<int64_t>(kLpPieceChunks, w.c1 - c0));
-            mbar_arrive_expect_tx(&sh.full[s], bytes);
-            bulk_g2s(ring + s * kLpPieceBytes, r.base + 16 * c0, bytes, &sh.full[s]);
-          }
-        }
-        if (*abort_flag) break;
-        kind = next;
-      }
-      if (*abort_flag) {  // the copies still in flight land before the CTA exits
-        for (uint32_t k = (n > kSlots ? n - kSlots : 0); k < n; ++k)
-          (void)mbar_wait(&sh.full[k % kSlots], (k / kSlots) & 1);
-      }
-    }
+  // the first loads start before it is known whether the row counts
+  uint4 qa[kBatch], qb[kBatch];
+  int c0 = warp * kBatchChunks;
+  load(qa, c0);
+  const int kind = row_kind(a, row);
+  if (kind <= 0) {
+    if (!a.part && warp == 0) write_no_row(a.lp, row, kind);
     return;
   }
-
-  if (warp > kLpWarps) {
-    // ---------------- finalizers ----------------
-    const uint32_t f = warp - kLpWarps - 1;
-    uint32_t k = 0, i = 0;  // units that count, units
-    int kind = kind_of(first);
-    for (int64_t u = first; u < units; u += G, ++i) {
-      const int next = kind_of(u + G);
-      if (kind <= 0) {
-        if (!a.part && i % kLpFinalizers == f) write_no_row(a.lp, unit_row(a, u), kind);
-        kind = next;
-        continue;
-      }
-      kind = next;
-      if (k % kLpFinalizers != f) {
-        ++k;
-        continue;
-      }
-      const int64_t row = unit_row(a, u);
-      const RowGeo r = row_geo<ES>(a.logits, row, a.ld, a.V);
-      const Unit w = unit_of(a, u, row, r);
-      int64_t e = edge_element(r, a.V, lane);
-      if (lane < 16 ? w.slice != 0 : w.slice != a.slices - 1) e = -1;
-      const float edge = e >= 0 ? Elem<T>::load(r.src + e * ES) : kNegInf;
-      float xt = 0.0f;
-      if (!a.part) xt = Elem<T>::load(r.src + a.lp.index[row] * ES);
-      const bool ok = __all_sync(0xffffffffu, wait(&sh.rowfull[f], (k / kLpFinalizers) & 1));
-      ++k;
-      if (!ok) break;
-      // this lane's 16 thread states, largest reference first
-      SoftState st = state_of_element(edge, a.c);
-      float m = st.r;
-      float2 rs[kLpWarps];
-#pragma unroll
-      for (int v = 0; v < kLpWarps; ++v) {
-        rs[v] = sh.part_rs[f][v][lane];
-        m = fmaxf(m, rs[v].x);
-      }
-      rescale(st, m);
-#pragma unroll
-      for (int v = 0; v < kLpWarps; ++v) {
-        SoftState o{rs[v].x, rs[v].y, ENT ? sh.part_t[f][v][lane] : 0.0f};
-        rescale(o, m);
-        st.s += o.s;
-        st.t += o.t;
-      }
-      st = warp_combine(st);
-      WarpTopK top{};
-      if constexpr (TOPK) {
-        uint32_t* keys = seg_keys + f * a.seg_cap;
-        const int segs = static_cast<int>((w.c1 - w.c0 + kSegChunks - 1) / kSegChunks);
-        for (int j = segs + lane; j < (segs + 127) / 128 * 128; j += 32) keys[j] = 0;
-        __syncwarp();
-        uint32_t thr;
-        const int n = pick_segments<T>(keys, segs, a.top_k, tsh.list[f], &thr);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.rowempty[f]);
-        top.buf = tsh.buf[f];
-        top.out = tsh.out[f];
-        top.k = a.top_k;
-        top.n = 0;
-        top.thr = thr ? (static_cast<uint64_t>(thr) << 32) - 1 : 0;
-        push_segments<T>(top, r, w, tsh.list[f], n);
-        top.push(rank_key(order_key(edge), e), e >= 0);
-        top.cut();
-      } else {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.rowempty[f]);
-      }
-      if (a.part) {
-        if (lane == 0) a.part[u] = make_float4(st.r, st.s, st.t, 0.0f);
-        if constexpr (TOPK)
-          for (int j = lane; j < a.top_k; j += 32) a.part_keys[u * a.top_k + j] = j < top.n ? top.out[j] : 0;
-      } else {
-        write_row<T>(a.lp, row, row_dist<T>(st, r.src, a.V, a.c), xt, TOPK ? top.out : nullptr);
-      }
-      __syncwarp();
-    }
-    return;
+  // the last warp takes the ragged ends, and with them the row's values
+  constexpr int kEnds = kLpWarps - 1;
+  int64_t e = -1;
+  float edge = kNegInf, xt = 0.0f;
+  if (warp == kEnds) {
+    e = edge_element(r, a.V, lane);
+    if (lane < 16 ? w.slice != 0 : w.slice != a.slices - 1) e = -1;
+    if (e >= 0) edge = Elem<T>::load(r.src + e * ES);
+    if (!a.part) xt = Elem<T>::load(r.src + a.lp.index[row] * ES);
   }
 
-  // ---------------- consumers ----------------
-  const int grp = warp / kLpGroupWarps;
-  const int gtid = static_cast<int>(threadIdx.x) - grp * kLpGroupThreads;
-  constexpr uint32_t kGroupSlots = kSlots / kLpGroups;  // a group's slots: grp, grp + 4, ...
-  static_assert(kSlots % kLpGroups == 0, "a slot always serves the same group");
-  uint32_t turn = static_cast<uint32_t>(grp);  // pieces of this unit before the group's next one
-  uint32_t gs = 0, gphase = 0;                 // the group's next slot and its phase
-  uint32_t j = 0, jphase = 1;                  // the unit's state buffer and its phase
-  // chunk i ^ (gtid % 8) of the thread's segment: eight threads' loads of 16
-  // bytes then fall into different banks
-  const uint32_t swz = static_cast<uint32_t>(gtid & 7);
-  const uint8_t* const my_seg = ring + grp * kLpPieceBytes + 128 * gtid + 16 * swz;
-  int kind = kind_of(first);
-  for (int64_t u = first; u < units; u += G) {
-    const int next = kind_of(u + G);
-    if (kind <= 0) {
-      kind = next;
-      continue;
+  WarpSums sums{kNegInf, kNegInf, {}, {}};
+  auto fold = [&](const uint4 (&q)[kBatch], int c0) {
+    float m[kBatch];
+    fold_batch<T, ENT, TOPK>(sums, q, a.c, a.low, m);
+    if constexpr (TOPK) {
+      static_assert(kBatch == 4, "one lane stores each segment's key");
+      const float mine = lane == 0 ? m[0] : lane == 1 ? m[1] : lane == 2 ? m[2] : m[3];
+      if (lane < kBatch) seg_keys[c0 / kSegChunks + lane] = order_key(mine);
     }
-    kind = next;
-    const int nc_all = unit_chunks<ES>(a, u);
-    const uint32_t np = static_cast<uint32_t>(nc_all + kLpPieceChunks - 1) / kLpPieceChunks;
-    // the unit's states and keys go where unit k - 4's were
-    bool ok = true;
-    if (lane == 0) ok = wait(&sh.rowempty[j], jphase);
-    if (!__all_sync(0xffffffffu, ok)) break;
-    SoftState st{kNegInf, 0.0f, 0.0f};
-    for (; turn < np; turn += kLpGroups) {
-      const uint32_t s = gs * kLpGroups + grp;
-      if (!__all_sync(0xffffffffu, wait(&sh.full[s], gphase))) {
-        ok = false;
-        break;
-      }
-      const uint8_t* seg = my_seg + gs * (kLpGroups * kLpPieceBytes);
-      if (++gs == kGroupSlots) {
-        gs = 0;
-        gphase ^= 1;
-      }
-      const int nc = nc_all - static_cast<int>(turn) * kLpPieceChunks - kSegChunks * gtid;
-      uint4 q[kSegChunks];
+  };
+  constexpr int kStep = kLpWarps * kBatchChunks;
+  while (c0 < nc) {
+    if (c0 + kStep < nc) load(qb, c0 + kStep);
+    fold(qa, c0);
+    c0 += kStep;
+    if (c0 >= nc) break;
+    if (c0 + kStep < nc) load(qa, c0 + kStep);
+    fold(qb, c0);
+    c0 += kStep;
+  }
+  const float2 sa = __fadd2_rn(sums.s[0], sums.s[1]), ta = __fadd2_rn(sums.t[0], sums.t[1]);
+  SoftState st{sums.r, sa.x + sa.y, ta.x + ta.y};
 #pragma unroll
-      for (int i = 0; i < kSegChunks; ++i)
-        q[i] = *reinterpret_cast<const uint4*>(seg + (static_cast<int>((i ^ swz)) - static_cast<int>(swz)) * 16);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.empty[s]);
-      if (nc < kSegChunks) {  // a row's last piece: no chunks there
-        const uint32_t none = ES == 2 ? 0xff80ff80u : 0xff800000u;
-#pragma unroll
-        for (int i = 0; i < kSegChunks; ++i)
-          if (static_cast<int>(i ^ swz) >= nc) q[i] = make_uint4(none, none, none, none);
-      }
-      if (nc > 0) {
-        const float cm = fold_segment<T, ENT>(st, q, a.c, a.low);
-        if constexpr (TOPK) seg_keys[j * a.seg_cap + turn * kPieceSegs + gtid] = order_key(cm);
-      }
-    }
-    if (!ok) break;
-    turn -= np;
-    sh.part_rs[j][warp][lane] = make_float2(st.r, st.s);
-    if constexpr (ENT) sh.part_t[j][warp][lane] = st.t;
+  for (int o = 16; o > 0; o >>= 1) {
+    st.s += __shfl_xor_sync(0xffffffffu, st.s, o);
+    if (ENT) st.t += __shfl_xor_sync(0xffffffffu, st.t, o);
+  }
+  if (warp == kEnds) st = combine(st, warp_combine(state_of_element(edge, a.c)));
+  if (lane == 0) sh.state[warp] = make_float4(st.r, st.s, st.t, 0.0f);
+  if (TOPK && tid == 0) sh.count = 0;
+  __syncthreads();
+  const int segs = (nc + kSegChunks - 1) / kSegChunks;
+  if (TOPK && warp == 0) {
+    // keys to a multiple of 128 (the last batch's are there already)
+    for (int j = segs + lane; j < (segs + 127) / 128 * 128; j += 32) seg_keys[j] = 0;
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.rowfull[j]);
-    if (++j == kLpFinalizers) {
-      j = 0;
-      jphase ^= 1;
+    uint32_t thr;
+    const int n = pick_segments<T>(seg_keys, segs, a.top_k, sh.list, &thr);
+    if (lane == 0) {
+      sh.listed = n;
+      sh.least = least_of<T>(thr);
+    }
+  }
+  if (warp == kEnds) {
+    SoftState all{kNegInf, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < kLpWarps; ++i) {
+      const float4 v = sh.state[i];
+      all = combine(all, SoftState{v.x, v.y, v.z});
+    }
+    if (a.part) {
+      if (lane == 0) a.part[u] = make_float4(all.r, all.s, all.t, 0.0f);
+    } else {
+      const RowDist d = row_dist<T>(all, r.src, a.V, a.c);
+      if (lane == 0) {
+        write_values<T>(a.lp, row, d, xt);
+        if (TOPK) sh.dist = d;
+      }
+    }
+  }
+  if constexpr (TOPK) {
+    __syncthreads();
+    const int listed = sh.listed;
+    const float least = sh.least;
+    auto offer = [&](float x, int64_t j) {
+      const int p = atomicAdd(&sh.count, 1);
+      if (p < kCandidates) tsh.buf[p] = rank_key(order_key(x), j);
+    };
+    constexpr int kAhead = 4;
+    for (int i0 = warp; i0 < listed; i0 += kLpWarps * kAhead) {
+      uint4 q[kAhead];
+      int c[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int at = i0 + i * kLpWarps;
+        c[i] = at < listed ? sh.list[at] * kSegChunks + lane : nc;
+        if (c[i] < nc) q[i] = __ldcg(chunks - lane + c[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (c[i] >= nc) continue;
+        uint32_t hits = reach_mask<T>(q[i], least);
+        if (hits == 0) continue;
+        float v[EPC];
+        unpack16<T>(q[i], v);
+        const int64_t j0 = (16 * (w.c0 + c[i]) - r.lead) / ES;
+        while (hits) {
+          const int j = __ffs(hits) - 1;
+          hits &= hits - 1;
+          float x = v[0];
+#pragma unroll
+          for (int k = 1; k < EPC; ++k) x = j == k ? v[k] : x;
+          offer(x, j0 + j);
+        }
+      }
+    }
+    if (e >= 0 && edge >= least) offer(edge, e);
+    __syncthreads();
+    int n = sh.count;
+    if (n > kCandidates) {  // the same n in every thread
+      __syncthreads();
+      if (warp == kEnds) {
+        n = pick_slowly<T>(tsh, r, w, sh.list, listed, a.top_k, edge, e);
+        if (lane == 0) sh.count = n;
+      }
+      __syncthreads();
+      n = sh.count;
+    }
+    // each key's place is the number of larger keys (keys are distinct, so
+    // the order of the offers does not matter)
+    const RowDist d = sh.dist;
+    for (int i = tid; i < n; i += kLpThreads) {
+      const uint64_t key = tsh.buf[i];
+      int above = 0;
+      for (int j = 0; j < n; ++j) above += tsh.buf[j] > key ? 1 : 0;
+      if (above >= a.top_k) continue;
+      if (a.part) a.part_keys[u * a.top_k + above] = key;
+      else write_top<T>(a.lp, row, d, above, key);
+    }
+    // a slice, or a row without a distribution, may have fewer
+    for (int i = tmin(n, a.top_k) + tid; i < a.top_k; i += kLpThreads) {
+      if (a.part) a.part_keys[u * a.top_k + i] = 0;
+      else write_top<T>(a.lp, row, d, i, 0);
     }
   }
 }
@@ -582,7 +574,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) logprobs_merge_kernel(StatAr
       }
       top.cut();
     }
-    write_row<T>(a.lp, row, row_dist<T>(st, src, a.V, a.c), xt, top.out);
+    const RowDist d = row_dist<T>(st, src, a.V, a.c);
+    if (lane == 0) write_values<T>(a.lp, row, d, xt);
+    for (int k = lane; k < a.top_k; k += 32) write_top<T>(a.lp, row, d, k, k < top.n ? top.out[k] : 0);
     __syncwarp();
   }
 }
@@ -744,21 +738,20 @@ int token_sm_count() {
   return n > 0 ? n : 148;
 }
 
-// Slices per row.  One unit costs its segments plus about 64 (a unit's fixed
-// work), the merge about 850 (2.5 us at an SM's share of the copy rate); the
-// busiest SM's total decides.  With alternatives a unit's keys fit shared memory.
-int plan_slices(int64_t B, int64_t V, int es, bool topk, int sms) {
-  const int64_t segs = (V * es + 16 * kSegChunks - 1) / (16 * kSegChunks) + 1;
-  const int64_t lo = topk ? (segs + kLpMaxSegs - 1) / kLpMaxSegs : 1;
-  const int64_t hi = tmax<int64_t>(lo, tmin<int64_t>(64, segs / kPieceSegs));
+// Slices per row.  CTAs of a wave share the SMs; a unit costs its segments
+// plus about 24 (a unit's fixed work), the merge about 200 (2.5 us).  With
+// alternatives a unit has at most kLpMaxSegs segments.
+int plan_slices(int64_t B, int64_t segs, bool topk, int64_t resident) {
+  const int64_t lo = topk ? tmax<int64_t>(1, (segs + kLpMaxSegs - 1) / kLpMaxSegs) : 1;
+  const int64_t hi = tmax<int64_t>(lo, tmin<int64_t>(64, segs / kBatch));
   int64_t best = lo, cost = INT64_MAX;
   for (int64_t s = lo; s <= hi; ++s) {
-    const int64_t c = ((B * s + sms - 1) / sms) * ((segs + s - 1) / s + 64) + (s > 1 ? 850 : 0);
+    const int64_t c = ((B * s + resident - 1) / resident) * ((segs + s - 1) / s + 24) + (s > 1 ? 200 : 0);
     if (c < cost) {
       cost = c;
       best = s;
     }
-    if (B >= 64 * sms) break;
+    if (B >= 8 * resident) break;
   }
   return static_cast<int>(best);
 }
@@ -767,8 +760,8 @@ using StatKernel = void (*)(StatArgs);
 
 template <bool ENT, bool TOPK>
 StatKernel stat_kernel(int es) {
-  return es == 4 ? static_cast<StatKernel>(logprobs_ring_kernel<float, ENT, TOPK>)
-                 : static_cast<StatKernel>(logprobs_ring_kernel<uint16_t, ENT, TOPK>);
+  return es == 4 ? static_cast<StatKernel>(logprobs_kernel<float, ENT, TOPK>)
+                 : static_cast<StatKernel>(logprobs_kernel<uint16_t, ENT, TOPK>);
 }
 
 // The lowest logit that keeps x c finite, as packed bf16 or fp32 bits.
@@ -794,11 +787,12 @@ gh_status_t logprobs_launch(const LogprobArgs& o, gh_dtype_t dtype, cudaStream_t
   a.low = low_bits(o.c, es);
   a.top_k = o.top_k;
   a.lp = o;
-  a.slices = plan_slices(o.B, o.V, es, topk, sms);
-  const int64_t segs = (o.V * es + 127) / 128 + 1;
-  a.slice_segs = static_cast<int>((segs + a.slices - 1) / a.slices);
-  a.seg_cap = (a.slice_segs + 127) / 128 * 128;
+  constexpr int kResident = 8;  // CTAs of an SM
+  const int64_t segs = (o.V * es / 16 + kSegChunks - 1) / kSegChunks;
+  a.slices = plan_slices(o.B, segs, topk, static_cast<int64_t>(sms) * kResident);
+  a.slice_segs = static_cast<int>(tmax<int64_t>(1, (segs + a.slices - 1) / a.slices));
   const int64_t units = o.B * a.slices;
+  if (units > INT32_MAX) return GH_ERR_UNSUPPORTED;  // one CTA each
 
   void* scratch = nullptr;
   if (a.slices > 1) {
@@ -808,13 +802,12 @@ gh_status_t logprobs_launch(const LogprobArgs& o, gh_dtype_t dtype, cudaStream_t
     a.part_keys = reinterpret_cast<uint64_t*>(static_cast<char*>(scratch) + units * 16);
   }
   const StatKernel kern = topk ? stat_kernel<true, true>(es) : stat_kernel<true, false>(es);
-  const int smem = topk ? lp_smem_bytes<true>(a.seg_cap) : lp_smem_bytes<false>(0);
-  gh_status_t st = ensure_smem_limit(kern, topk ? lp_smem_bytes<true>(kLpMaxSegs) : smem) == cudaSuccess ? GH_OK : GH_ERR_CUDA;
-  if (st == GH_OK) {
+  const int smem = topk ? (a.slice_segs + 127) / 128 * 128 * 4 : 0;
+  gh_status_t st = GH_OK;
+  {
     ProfileScope prof(GH_KERNEL_LOGPROBS, stream);
     note_launch();
-    if (launch_pdl(kern, dim3(static_cast<unsigned>(tmin<int64_t>(units, sms))), dim3(kLpThreads), smem, stream, 1, a) !=
-        cudaSuccess)
+    if (launch_pdl(kern, dim3(static_cast<unsigned>(units)), dim3(kLpThreads), smem, stream, 1, a) != cudaSuccess)
       st = GH_ERR_CUDA;
     if (st == GH_OK && a.slices > 1) {
       const unsigned grid = static_cast<unsigned>(tmin<int64_t>((o.B + kMergeWarps - 1) / kMergeWarps, 8 * sms));

@@ -32,8 +32,7 @@ struct StatArgs {
   float c;             // log2(e) / temperature
   uint32_t low;        // lowest logit whose x c is finite (packed bf16, or fp32 bits)
   int slices;          // per row
-  int slice_segs;      // 128-byte segments per slice
-  int seg_cap;         // keys kept per unit, a multiple of 128
+  int slice_segs;      // 512-byte segments per slice
   int top_k;
   const int8_t* flags; // [B] 1: the row counts (null: by lp.index)
   float4* part;        // [B * slices] (reference, sum, weighted sum, -)
