@@ -347,16 +347,6 @@ gh_status_t gh_topk_distill(const void* logits, int64_t ld, const int64_t* teach
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   if (B == 0) return cudaMemsetAsync(loss, 0, sizeof(float), stream) == cudaSuccess ? GH_OK : GH_ERR_CUDA;
 
-  // Scratch: the count, and the row losses unless the caller takes them.
-  void* scratch = nullptr;
-  const size_t rows_bytes = row_loss_out ? 0 : static_cast<size_t>(B) * sizeof(float);
-  gh_status_t st = scratch_alloc(&scratch, 16 + rows_bytes, stream);
-  if (st != GH_OK) return st;
-  unsigned long long* counter = static_cast<unsigned long long*>(scratch);
-  float* row_loss = row_loss_out ? row_loss_out : reinterpret_cast<float*>(static_cast<char*>(scratch) + 16);
-  const unsigned long long* n_valid =
-      n_valid_total ? reinterpret_cast<const unsigned long long*>(n_valid_total) : counter;
-  const int mean = reduction == GH_REDUCTION_MEAN;
   DistillArgs a{};
   a.logits = logits;
   a.grad = grad;
@@ -370,14 +360,10 @@ gh_status_t gh_topk_distill(const void* logits, int64_t ld, const int64_t* teach
   a.temperature = temperature;
   a.c = static_cast<float>(1.4426950408889634 / static_cast<double>(temperature));
   a.renormalize = renormalize;
-  a.mean = mean;
-  a.n_valid = n_valid;
-  a.row_loss = row_loss;
-  if (!n_valid_total) st = distill_count_launch(teacher_index, teacher_logits, B, a.K, V, counter, stream);
-  if (st == GH_OK) st = distill_launch(a, dtype, stream);
-  if (st == GH_OK) st = ce_reduce_launch(row_loss, B, n_valid, mean, loss, stream);
-  scratch_free(scratch, stream);
-  return st;
+  a.mean = reduction == GH_REDUCTION_MEAN;
+  a.n_valid = reinterpret_cast<const unsigned long long*>(n_valid_total);
+  a.row_loss = row_loss_out;
+  return distill_launch(a, dtype, loss, stream);
 }
 
 static gh_status_t linear_ce_impl(const void* inputs, const void* weight, const int64_t* targets, int64_t N,

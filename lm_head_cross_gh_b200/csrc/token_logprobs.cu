@@ -46,9 +46,6 @@ namespace {
 
 constexpr int kLpWarps = 4;
 constexpr int kLpThreads = 32 * kLpWarps;
-constexpr int kBatch = 4;
-constexpr int kSegChunks = 32;  // 512 bytes
-constexpr int kBatchChunks = kBatch * kSegChunks;
 constexpr int kLpMaxSegs = 2048;  // segments of a unit whose keys are kept (8 KiB)
 constexpr int kCandidates = 512;  // logits of the picked segments that reach the threshold, before the slow way
 
@@ -64,125 +61,6 @@ struct LpTopShared {
   uint64_t out[GH_MAX_TOP_K];
 };
 static_assert(kCandidates >= kTopBuf, "the slow way's buffer");
-
-__device__ __forceinline__ uint32_t bf16x2_max_nan(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ float f32_max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
-
-template <typename T>
-__device__ __forceinline__ uint4 max4(const uint4& a, const uint4& b);
-template <>
-__device__ __forceinline__ uint4 max4<uint16_t>(const uint4& a, const uint4& b) {
-  return make_uint4(bf16x2_max_nan(a.x, b.x), bf16x2_max_nan(a.y, b.y), bf16x2_max_nan(a.z, b.z),
-                    bf16x2_max_nan(a.w, b.w));
-}
-template <>
-__device__ __forceinline__ uint4 max4<float>(const uint4& a, const uint4& b) {
-  return make_uint4(__float_as_uint(f32_max_nan(__uint_as_float(a.x), __uint_as_float(b.x))),
-                    __float_as_uint(f32_max_nan(__uint_as_float(a.y), __uint_as_float(b.y))),
-                    __float_as_uint(f32_max_nan(__uint_as_float(a.z), __uint_as_float(b.z))),
-                    __float_as_uint(f32_max_nan(__uint_as_float(a.w), __uint_as_float(b.w))));
-}
-// Largest element of a chunk; NaN if there is one.
-template <typename T>
-__device__ __forceinline__ float max_of4(const uint4& q);
-template <>
-__device__ __forceinline__ float max_of4<uint16_t>(const uint4& q) {
-  const uint32_t m = bf16x2_max_nan(bf16x2_max_nan(q.x, q.y), bf16x2_max_nan(q.z, q.w));
-  return f32_max_nan(bf16_lo(m), bf16_hi(m));
-}
-template <>
-__device__ __forceinline__ float max_of4<float>(const uint4& q) {
-  return f32_max_nan(f32_max_nan(__uint_as_float(q.x), __uint_as_float(q.y)),
-                     f32_max_nan(__uint_as_float(q.z), __uint_as_float(q.w)));
-}
-
-// Logits below `low` add nothing to a row of |R| <= kFarRef; raised to it they
-// keep y finite, so that 0 y = 0 in t.
-template <typename T>
-__device__ __forceinline__ uint4 clamp_low(const uint4& q, uint32_t low);
-template <>
-__device__ __forceinline__ uint4 clamp_low<uint16_t>(const uint4& q, uint32_t low) {
-  return make_uint4(bf16x2_max(q.x, low), bf16x2_max(q.y, low), bf16x2_max(q.z, low), bf16x2_max(q.w, low));
-}
-template <>
-__device__ __forceinline__ uint4 clamp_low<float>(const uint4& q, uint32_t low) {
-  const float l = __uint_as_float(low);
-  return make_uint4(__float_as_uint(fmaxf(__uint_as_float(q.x), l)), __float_as_uint(fmaxf(__uint_as_float(q.y), l)),
-                    __float_as_uint(fmaxf(__uint_as_float(q.z), l)), __float_as_uint(fmaxf(__uint_as_float(q.w), l)));
-}
-
-// Largest of the warp's values; NaN if there is one.
-__device__ __forceinline__ float warp_max_nan(float v) {
-  float d;
-  asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(v));
-  return d;
-}
-
-// A warp's running sums: one reference for its lanes (the largest logit so
-// far), so it rises seldom and the lanes' sums add without rescaling.
-struct WarpSums {
-  float m;         // largest logit so far (-inf: none; +inf: a NaN or +inf was seen)
-  float r;         // its reference, ref_of(m)
-  float2 s[2], t[2];
-};
-
-// A batch's largest logit is `m` (NaN if it has one): raise the reference.
-__device__ __forceinline__ void raise(WarpSums& w, float m, float c) {
-  const float top = m < kPosInf ? m : kPosInf;
-  const float r = ref_of(top, c);
-  const bool sums = fabsf(w.r) <= kFarRef;  // else there is nothing to rescale yet
-  const float d = sums ? fmaxf(w.r - r, -2.0f * kFarRef) : 0.0f, f = ex2(d);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    w.t[i] = make_float2(f * fmaf(w.s[i].x, d, w.t[i].x), f * fmaf(w.s[i].y, d, w.t[i].y));
-    w.s[i] = make_float2(f * w.s[i].x, f * w.s[i].y);
-  }
-  w.m = top;
-  w.r = r;
-}
-
-// Folds a lane's chunks of a batch into its warp's sums.  TOPK: the segments'
-// largest logits go to m[].
-template <typename T, bool ENT, bool TOPK>
-__device__ __forceinline__ void fold_batch(WarpSums& w, const uint4 (&q)[kBatch], float c, uint32_t low,
-                                           float (&m)[kBatch]) {
-  constexpr int EPC = 16 / Elem<T>::kBytes;
-  float bm;
-  if constexpr (TOPK) {
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) m[i] = warp_max_nan(max_of4<T>(q[i]));
-    bm = f32_max_nan(f32_max_nan(m[0], m[1]), f32_max_nan(m[2], m[3]));
-  } else {
-    bm = warp_max_nan(max_of4<T>(max4<T>(max4<T>(q[0], q[1]), max4<T>(q[2], q[3]))));
-  }
-  if (!(bm <= w.m)) raise(w, bm, c);
-  if (!(fabsf(w.r) <= kFarRef)) return;
-  const float2 c2 = make_float2(c, c), nr = make_float2(-w.r, -w.r);
-#pragma unroll
-  for (int i = 0; i < kBatch; ++i) {
-    float v[EPC];
-    unpack16<T>(ENT ? clamp_low<T>(q[i], low) : q[i], v);
-#pragma unroll
-    for (int j = 0; j < EPC; j += 2) {
-      const float2 y = __ffma2_rn(make_float2(v[j], v[j + 1]), c2, nr);
-      const float2 e = make_float2(ex2(y.x), ex2(y.y));
-      float2& a = w.s[(j / 2) & 1];
-      a = __fadd2_rn(a, e);
-      if constexpr (ENT) {
-        float2& b = w.t[(j / 2) & 1];
-        b = __ffma2_rn(e, y, b);
-      }
-    }
-  }
-}
 
 // Where unit u lies: row, slice, and its chunks of the row.
 struct Unit {

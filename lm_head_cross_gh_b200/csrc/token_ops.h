@@ -62,8 +62,14 @@ struct DistillArgs {
   float c;       // log2(e) / temperature
   int renormalize;
   int mean;
-  const unsigned long long* n_valid;  // rows with an entry (of the whole batch)
-  float* row_loss;                    // [B]
+  const unsigned long long* n_valid;  // rows with an entry, of the whole batch (null: counted here)
+  float* row_loss;                    // [B] (null: scratch)
+  // set by distill_launch
+  unsigned int* parts;        // counts of rows with an entry, to be added
+  int nparts;
+  int8_t* flags;              // [B] 1: the row has an entry
+  int cluster;                // CTAs per row
+  int64_t slice_chunks;       // 16-byte chunks per CTA of a row
 };
 
 gh_status_t logprobs_launch(const LogprobArgs& a, gh_dtype_t dtype, cudaStream_t stream);
@@ -71,6 +77,7 @@ gh_status_t logprobs_vjp_launch(const LogprobVjpArgs& a, gh_dtype_t dtype, cudaS
 // Counts the rows with an entry into *count (written, not added to).
 gh_status_t distill_count_launch(const int64_t* ids, const float* values, int64_t B, int K, int64_t V,
                                  unsigned long long* count, cudaStream_t stream);
-gh_status_t distill_launch(const DistillArgs& a, gh_dtype_t dtype, cudaStream_t stream);
+// Writes the scalar loss, the row losses and, with a.grad, the gradient.
+gh_status_t distill_launch(const DistillArgs& a, gh_dtype_t dtype, float* loss, cudaStream_t stream);
 
 }  // namespace gh

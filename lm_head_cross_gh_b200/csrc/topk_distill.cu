@@ -9,132 +9,384 @@
 // (the T^2 keeps the gradient's size as T grows).  An entry whose id is -1 or
 // whose value is -inf is none; a row without entries has no loss and a zero
 // gradient.
+//
+// distill_kernel: 15 streaming warps and one for the teacher's side per row, or a cluster of CTAs for long rows and
+// small batches.  The first pass sums 2^(x c - R) as the log-probabilities'
+// forward does; the second reads the row again, from L2 (the rows in flight,
+// two per SM, are far smaller), and stores the dense part scale T Q p_j; then
+// one warp, which has worked out the teacher's side meanwhile, stores the K
+// elements that differ.  HBM sees one read and one write of every logit.
 #include "ce.h"
-#include "ce_device.cuh"
-#include "common.cuh"
+#include "linear_ce.h"
 #include "profile.h"
+#include "token_device.cuh"
 #include "token_ops.h"
 
 namespace gh {
 
 namespace {
 
-constexpr int kDistillThreads = 512;
+constexpr int kDistillWarps = 15;  // that stream the row; one more has the teacher's side
+constexpr int kDistillThreads = 32 * (kDistillWarps + 1);
+constexpr int kLaneEntries = GH_MAX_TOP_K / 32;
+constexpr int kCountParts = 64;  // CTAs of the counting kernel
 
 __device__ __forceinline__ bool distill_entry(int64_t id, float v, int64_t V) {
   return id >= 0 && id < V && !(v == kNegInf);
 }
 
-// Rows with at least one entry; one warp per row, one CTA, no atomics.
-__global__ void __launch_bounds__(1024) distill_count_kernel(const int64_t* __restrict__ ids,
-                                                             const float* __restrict__ values, int64_t B, int K,
-                                                             int64_t V, unsigned long long* count) {
-  __shared__ unsigned long long part[32];
+// Which rows have an entry (flags, optional), and how many: each CTA writes its
+// own count to parts[blockIdx.x], or adds it to *total.
+__global__ void __launch_bounds__(256) distill_count_kernel(const int64_t* __restrict__ ids,
+                                                            const float* __restrict__ values, int64_t B, int K,
+                                                            int64_t V, int8_t* flags, unsigned int* parts,
+                                                            unsigned long long* total) {
+  __shared__ unsigned int n_sh;
   pdl_wait();
   pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  unsigned long long n = 0;
-  for (int64_t row = warp; row < B; row += 32) {
+  if (threadIdx.x == 0) n_sh = 0;
+  __syncthreads();
+  const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
+  unsigned int n = 0;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + warp; row < B; row += static_cast<int64_t>(gridDim.x) * 8) {
     bool any = false;
-    for (int k = lane; k < K; k += 32) {
-      const int64_t id = ids[row * K + k];
-      any |= distill_entry(id, values[row * K + k], V);
+    for (int k0 = 0; k0 < K && !any; k0 += 32) {
+      const int k = k0 + lane;
+      const bool has = k < K && distill_entry(ids[row * K + k], values[row * K + k], V);
+      any = __any_sync(0xffffffffu, has);
     }
-    n += __any_sync(0xffffffffu, any) ? 1 : 0;
+    n += any ? 1 : 0;
+    if (flags && lane == 0) flags[row] = any ? 1 : 0;
   }
-  if (lane == 0) part[warp] = n;
+  if (lane == 0) atomicAdd(&n_sh, n);
   __syncthreads();
   if (threadIdx.x == 0) {
-    unsigned long long tot = 0;
-    for (int w = 0; w < 32; ++w) tot += part[w];
-    *count = tot;
+    if (parts) parts[blockIdx.x] = n_sh;
+    else atomicAdd(total, static_cast<unsigned long long>(n_sh));
   }
 }
 
+// 1 / max(n, 1) of a mean, n given or the sum of the counting kernel's parts
+// (by one warp; the same in every lane).
+__device__ __forceinline__ float distill_scale(const DistillArgs& a, int lane) {
+  if (!a.mean) return 1.0f;
+  unsigned long long n = 0;
+  if (a.n_valid) {
+    n = *a.n_valid;
+  } else {
+    unsigned int m = 0;
+    for (int i = lane; i < a.nparts; i += 32) m += a.parts[i];
+    n = __reduce_add_sync(0xffffffffu, m);
+  }
+  return 1.0f / static_cast<float>(n > 0 ? n : 1ull);
+}
+
+// The teacher's side of a row, by one warp: lane l has entries l, l + 32, ...
+struct Teacher {
+  int id[kLaneEntries];  // -1: none
+  float log_q[kLaneEntries], q[kLaneEntries];
+  float total;  // Q
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+__device__ __forceinline__ Teacher teacher_row(const DistillArgs& a, int64_t row, int lane, bool report) {
+  Teacher t;
+  float vm = kNegInf;
+#pragma unroll
+  for (int i = 0; i < kLaneEntries; ++i) {
+    const int k = lane + 32 * i;
+    t.id[i] = -1;
+    t.log_q[i] = kNegInf;
+    if (k < a.K) {
+      const int64_t id = a.ids[row * a.K + k];
+      const float v = a.values[row * a.K + k];
+      if (report && (id < -1 || id >= a.V)) record_status(GH_ERR_TARGET_RANGE);
+      if (distill_entry(id, v, a.V)) {
+        t.id[i] = static_cast<int>(id);
+        t.log_q[i] = v;
+        vm = fmaxf(vm, v);
+      }
+    }
+  }
+  float sum = 0.0f;
+  if (a.renormalize) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+#pragma unroll
+    for (int i = 0; i < kLaneEntries; ++i) {
+      t.log_q[i] = t.id[i] >= 0 ? (t.log_q[i] - vm) / a.temperature : kNegInf;
+      t.q[i] = t.id[i] >= 0 ? expf(t.log_q[i]) : 0.0f;
+      sum += t.q[i];
+    }
+    sum = warp_sum(sum);
+    const float log_sum = logf(sum);
+#pragma unroll
+    for (int i = 0; i < kLaneEntries; ++i) {
+      t.log_q[i] -= log_sum;
+      t.q[i] /= sum;
+    }
+    t.total = sum == sum ? 1.0f : sum;  // (a NaN value makes the row NaN)
+  } else {
+#pragma unroll
+    for (int i = 0; i < kLaneEntries; ++i) {
+      t.q[i] = t.id[i] >= 0 ? expf(t.log_q[i]) : 0.0f;
+      sum += t.q[i];
+    }
+    t.total = warp_sum(sum);
+  }
+  return t;
+}
+
+// Gradient of a chunk's dense part: coef 2^y, y = (x - sub) c - r.
+template <typename T, bool SUB>
+__device__ __forceinline__ void dense_chunk(const uint4& q, float sub, float c, float r, float coef, uint8_t* dst,
+                                            bool congruent) {
+  constexpr int ES = Elem<T>::kBytes, EPC = 16 / ES;
+  float v[EPC], g[EPC];
+  unpack16<T>(q, v);
+  const float2 c2 = make_float2(c, c), nr = make_float2(-r, -r), k2 = make_float2(coef, coef), s2 = make_float2(-sub, -sub);
+#pragma unroll
+  for (int j = 0; j < EPC; j += 2) {
+    float2 x = make_float2(v[j], v[j + 1]);
+    if (SUB) x = __fadd2_rn(x, s2);
+    const float2 y = __ffma2_rn(x, c2, nr);
+    const float2 e = __fmul2_rn(make_float2(ex2(y.x), ex2(y.y)), k2);
+    g[j] = e.x;
+    g[j + 1] = e.y;
+  }
+  if (congruent) {
+    __stcs(reinterpret_cast<uint4*>(dst), pack16<T>(g));
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPC; ++j) Elem<T>::store(dst + j * ES, g[j]);
+  }
+}
+
+struct DistillShared {
+  float2 state[kDistillWarps];  // the streaming warps' (reference, sum)
+  float2 part;                  // this CTA's, read by the cluster's others
+  RowDist dist;
+  float coef;
+};
+
 template <typename T>
-__global__ void __launch_bounds__(kDistillThreads) distill_kernel(DistillArgs a) {
+__global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(DistillArgs a) {
   constexpr int ES = Elem<T>::kBytes;
-  __shared__ float red[2][kDistillThreads / 32];
-  __shared__ float q_s[GH_MAX_TOP_K], fix_s[GH_MAX_TOP_K], tot_s[2];
-  __shared__ int64_t id_s[GH_MAX_TOP_K];
+  __shared__ DistillShared sh;
+  const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
+  const int tid = static_cast<int>(threadIdx.x);
   pdl_wait();
   pdl_trigger();
-  const int tid = static_cast<int>(threadIdx.x);
-  const unsigned long long nv = *a.n_valid;
-  const float scale = a.mean ? 1.0f / static_cast<float>(nv > 0 ? nv : 1ull) : 1.0f;
-  for (int64_t row = blockIdx.x; row < a.B; row += gridDim.x) {
-    const uint8_t* src = static_cast<const uint8_t*>(a.logits) + row * a.ld * ES;
-    uint8_t* dst = static_cast<uint8_t*>(a.grad) + row * a.ld_grad * ES;
-    __syncthreads();
-    // the entries; thread 0 computes q (K is at most 128)
-    if (tid < a.K) {
-      const int64_t id = a.ids[row * a.K + tid];
-      const float v = a.values[row * a.K + tid];
-      if (id < -1 || id >= a.V) record_status(GH_ERR_TARGET_RANGE);
-      id_s[tid] = distill_entry(id, v, a.V) ? id : -1;
-      q_s[tid] = v;
+  const int C = a.cluster;
+  const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int64_t row = C > 1 ? blockIdx.x / C : blockIdx.x;
+  const RowGeo r = row_geo<ES>(a.logits, row, a.ld, a.V);
+  // this CTA's chunks of the row, and the ragged ends with the first and last
+  const int64_t from = tmin(r.c_hi, r.c_lo + rank * a.slice_chunks);
+  const int nc = static_cast<int>((rank == C - 1 ? r.c_hi : tmin(r.c_hi, from + a.slice_chunks)) - from);
+  const uint4* const chunks = reinterpret_cast<const uint4*>(r.base) + from + lane;
+  uint8_t* const dst = static_cast<uint8_t*>(a.grad) + row * a.ld_grad * ES;
+  uint8_t* const gbase = dst - r.lead + 16 * from;  // this CTA's chunk i's gradient starts at gbase + 16 i
+  const bool congruent = ((reinterpret_cast<uintptr_t>(dst) ^ reinterpret_cast<uintptr_t>(r.src)) & 15) == 0;
+  constexpr int kStep = kDistillWarps * kBatchChunks;
+  const uint32_t none = ES == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
+  auto load = [&](uint4 (&q)[kBatch], int c0) {
+    if (c0 + kBatchChunks <= nc) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) q[i] = __ldcg(chunks + c0 + i * kSegChunks);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        q[i] = make_uint4(none, none, none, none);
+        if (c0 + i * kSegChunks + lane < nc) q[i] = __ldcg(chunks + c0 + i * kSegChunks);
+      }
     }
-    __syncthreads();
-    if (tid == 0) {
-      float vm = kNegInf, sum = 0.0f;
-      int n = 0;
-      for (int k = 0; k < a.K; ++k)
-        if (id_s[k] >= 0) {
-          ++n;
-          vm = fmaxf(vm, q_s[k]);
+  };
+  uint4 qa[kBatch], qb[kBatch];
+  const int first = warp < kDistillWarps ? warp * kBatchChunks : nc;
+  int c0 = first;
+  const bool counts = a.flags[row] != 0;
+  int64_t e = -1;  // a ragged-end element, in lanes of the last warp
+  constexpr int kEnds = kDistillWarps;
+  if (warp == kEnds) {
+    e = edge_element(r, a.V, lane);
+    if (lane < 16 ? rank != 0 : rank != C - 1) e = -1;
+  }
+  if (!counts) {
+    if (rank == 0 && tid == 0) a.row_loss[row] = 0.0f;
+    if (rank == 0 && warp == kEnds) (void)teacher_row(a, row, lane, true);
+    if (!a.grad) return;
+    for (int c = tid; c < nc; c += kDistillThreads) {
+      if (congruent) {
+        __stcs(reinterpret_cast<uint4*>(gbase + 16 * static_cast<int64_t>(c)), make_uint4(0, 0, 0, 0));
+      } else {
+        for (int j = 0; j < 16 / ES; ++j) Elem<T>::store(gbase + 16 * static_cast<int64_t>(c) + j * ES, 0.0f);
+      }
+    }
+    if (e >= 0) Elem<T>::store(dst + e * ES, 0.0f);
+    return;
+  }
+
+  // ---- first pass: the row's sum; the last warp also the teacher's side ----
+  load(qa, c0);
+  Teacher t;
+  float xk[kLaneEntries], edge = kNegInf, scale = 1.0f;
+  if (warp == kEnds) {
+    if (e >= 0) edge = Elem<T>::load(r.src + e * ES);
+    t = teacher_row(a, row, lane, rank == 0);
+#pragma unroll
+    for (int i = 0; i < kLaneEntries; ++i) xk[i] = t.id[i] >= 0 ? Elem<T>::load(r.src + static_cast<int64_t>(t.id[i]) * ES) : 0.0f;
+    scale = distill_scale(a, lane);
+  }
+  WarpSums sums{kNegInf, kNegInf, {}, {}};
+  float m_unused[kBatch];
+  while (c0 < nc) {
+    if (c0 + kStep < nc) load(qb, c0 + kStep);
+    fold_batch<T, false, false>(sums, qa, a.c, 0, m_unused);
+    c0 += kStep;
+    if (c0 >= nc) break;
+    if (c0 + kStep < nc) load(qa, c0 + kStep);
+    fold_batch<T, false, false>(sums, qb, a.c, 0, m_unused);
+    c0 += kStep;
+  }
+  // the second pass's first loads cross the exchange below
+  const bool with_grad = a.grad != nullptr;
+  c0 = first;
+  if (with_grad) load(qa, c0);
+  if (warp < kDistillWarps) {
+    const float2 sa = __fadd2_rn(sums.s[0], sums.s[1]);
+    const float s = warp_sum(sa.x + sa.y);
+    if (lane == 0) sh.state[warp] = make_float2(sums.r, s);
+  }
+  __syncthreads();
+  if (warp == kEnds || C > 1) {
+    SoftState st{kNegInf, 0.0f, 0.0f};
+    if (warp == kEnds) {
+      st = state_of_element(edge, a.c);
+      if (lane < kDistillWarps) st = combine(st, SoftState{sh.state[lane].x, sh.state[lane].y, 0.0f});
+      st = warp_combine(st);
+    }
+    if (C > 1) {
+      if (warp == kEnds && lane == 0) sh.part = make_float2(st.r, st.s);
+      __syncwarp();
+      cluster_arrive_release();
+      cluster_wait_acquire();
+      if (warp == kEnds) {
+        // every CTA merges the slices in the same order
+        st = {kNegInf, 0.0f, 0.0f};
+        for (int i = 0; i < C; ++i) {
+          const uint32_t p = map_to_rank(&sh.part, i);
+          st = combine(st, SoftState{ld_dsmem_f32(p), ld_dsmem_f32(p + 4), 0.0f});
         }
-      if (a.renormalize)
-        for (int k = 0; k < a.K; ++k)
-          if (id_s[k] >= 0) sum += expf((q_s[k] - vm) / a.temperature);
-      float Q = 0.0f;
-      for (int k = 0; k < a.K; ++k) {
-        const float lq = a.renormalize ? (q_s[k] - vm) / a.temperature - logf(sum) : q_s[k];
-        q_s[k] = lq;  // log q
-        if (id_s[k] >= 0) Q += expf(lq);
       }
-      tot_s[0] = n ? Q : -1.0f;
     }
-    __syncthreads();
-    const float Q = tot_s[0];
-    if (Q == -1.0f) {
-      if (tid == 0) a.row_loss[row] = 0.0f;
-      if (a.grad)
-        for (int64_t j = tid; j < a.V; j += kDistillThreads) Elem<T>::store(dst + j * ES, 0.0f);
-      continue;
-    }
-    float m = kNegInf;
-    for (int64_t j = tid; j < a.V; j += kDistillThreads) m = fmaxf(m, Elem<T>::load(src + j * ES));
-    m = block_max<kDistillThreads>(m, red[0]);
-    float s = 0.0f;
-    for (int64_t j = tid; j < a.V; j += kDistillThreads) s += ex2((Elem<T>::load(src + j * ES) - m) * a.c);
-    s = block_sum<kDistillThreads>(s, red[1]);
-    const float l2s = log2f(s);
-    const float ct = scale * a.temperature;
-    if (tid < a.K && id_s[tid] >= 0) {
-      // every entry with this id writes the same value: p Q less the q of all of them
-      const float y = (Elem<T>::load(src + id_s[tid] * ES) - m) * a.c;
-      float qs = 0.0f;
-      for (int k = 0; k < a.K; ++k)
-        if (id_s[k] == id_s[tid]) qs += expf(q_s[k]);
-      fix_s[tid] = ct * (Q * ex2(y) / s - qs);
-    }
-    if (tid == 0) {
-      float loss = 0.0f;
-      for (int k = 0; k < a.K; ++k) {
-        if (id_s[k] < 0) continue;
-        const float q = expf(q_s[k]);
-        const float y = (Elem<T>::load(src + id_s[k] * ES) - m) * a.c;
-        if (!(q == 0.0f)) loss += q * (q_s[k] - kLn2 * (y - l2s));
+    if (warp == kEnds) {
+      const RowDist d = row_dist<T>(st, r.src, a.V, a.c);
+      const float ct = scale * a.temperature;
+      if (lane == 0) {
+        sh.dist = d;
+        sh.coef = d.none ? kNaN : ct * t.total / d.s;
       }
-      a.row_loss[row] = a.temperature * a.temperature * loss;
+      if (rank == 0) {
+        float loss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kLaneEntries; ++i) {
+          const float lp = d.none ? kNaN : kLn2 * log2_p<T>(d, xk[i], a.c);
+          if (t.id[i] >= 0 && !(t.q[i] == 0.0f)) loss = fmaf(t.q[i], t.log_q[i] - lp, loss);
+        }
+        loss = warp_sum(loss);
+        if (lane == 0) a.row_loss[row] = a.temperature * a.temperature * loss;
+      }
+      if (with_grad) {
+        // the entries' elements: Q p less the q of every entry with this id
+        float qs[kLaneEntries];
+#pragma unroll
+        for (int i = 0; i < kLaneEntries; ++i) qs[i] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kLaneEntries; ++i) {
+          if (32 * i >= a.K) break;
+          for (int l = 0; l < tmin(32, a.K - 32 * i); ++l) {
+            const int id = __shfl_sync(0xffffffffu, t.id[i], l);
+            const float q = __shfl_sync(0xffffffffu, t.q[i], l);
+#pragma unroll
+            for (int j = 0; j < kLaneEntries; ++j) qs[j] += t.id[j] == id ? q : 0.0f;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kLaneEntries; ++i) {
+          const float p = d.none ? kNaN : ex2(fmaf(xk[i] - d.sub, a.c, -d.r)) / d.s;
+          xk[i] = ct * fmaf(t.total, p, -qs[i]);  // the gradient there
+        }
+      }
     }
-    if (!a.grad) continue;
-    __syncthreads();  // in place: the entries' logits are read before they are overwritten
-    const float coef = ct * Q / s;
-    for (int64_t j = tid; j < a.V; j += kDistillThreads)
-      Elem<T>::store(dst + j * ES, coef * ex2((Elem<T>::load(src + j * ES) - m) * a.c));
+  }
+  __syncthreads();
+  if (C > 1) {
+    // In place, no CTA stores before every other has read what it needs of the
+    // row; and none leaves before its state has been read.
+    cluster_arrive_release();
+    cluster_wait_acquire();
+  }
+
+  // ---- second pass: the dense gradient, then the entries' elements ----
+  if (with_grad) {
+    const RowDist d = sh.dist;
+    const float coef = sh.coef;
+    auto put = [&](const uint4 (&q)[kBatch], int at) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int c = at + i * kSegChunks + lane;
+        if (c >= nc) break;
+        uint8_t* p = gbase + 16 * static_cast<int64_t>(c);
+        if (d.sub == 0.0f) dense_chunk<T, false>(q[i], 0.0f, a.c, d.r, coef, p, congruent);
+        else dense_chunk<T, true>(q[i], d.sub, a.c, d.r, coef, p, congruent);
+      }
+    };
+    while (c0 < nc) {
+      if (c0 + kStep < nc) load(qb, c0 + kStep);
+      put(qa, c0);
+      c0 += kStep;
+      if (c0 >= nc) break;
+      if (c0 + kStep < nc) load(qa, c0 + kStep);
+      put(qb, c0);
+      c0 += kStep;
+    }
+    if (e >= 0) Elem<T>::store(dst + e * ES, coef * ex2(fmaf(edge - d.sub, a.c, -d.r)));
     __syncthreads();
-    if (tid < a.K && id_s[tid] >= 0) Elem<T>::store(dst + id_s[tid] * ES, fix_s[tid]);
+    if (warp == kEnds) {
+      // entries of this CTA's part of the row (in-place: their logits were read above)
+      const int64_t lo = rank == 0 ? 0 : (16 * from - r.lead) / ES;
+      const int64_t hi = rank == C - 1 ? a.V : (16 * (from + nc) - r.lead) / ES;
+#pragma unroll
+      for (int i = 0; i < kLaneEntries; ++i)
+        if (t.id[i] >= 0 && t.id[i] >= lo && t.id[i] < hi) Elem<T>::store(dst + static_cast<int64_t>(t.id[i]) * ES, xk[i]);
+    }
+  }
+}
+
+// Sum of the row losses in a fixed order, in double, and the mean's division.
+__global__ void __launch_bounds__(1024) distill_reduce_kernel(DistillArgs a, float* loss) {
+  __shared__ double red[32];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  double s = 0.0;
+  for (int64_t i = threadIdx.x; i < a.B; i += 1024) s += static_cast<double>(a.row_loss[i]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) red[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const double scale = static_cast<double>(distill_scale(a, lane));
+    s = red[lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) *loss = static_cast<float>(s * scale);
   }
 }
 
@@ -142,21 +394,59 @@ __global__ void __launch_bounds__(kDistillThreads) distill_kernel(DistillArgs a)
 
 gh_status_t distill_count_launch(const int64_t* ids, const float* values, int64_t B, int K, int64_t V,
                                  unsigned long long* count, cudaStream_t stream) {
+  if (cudaMemsetAsync(count, 0, sizeof(*count), stream) != cudaSuccess) return GH_ERR_CUDA;
+  const unsigned grid = static_cast<unsigned>(tmin<int64_t>((B + 7) / 8, kCountParts));
   note_launch();
-  return launch_pdl(distill_count_kernel, dim3(1), dim3(1024), 0, stream, 1, ids, values, B, K, V, count) ==
-                 cudaSuccess
+  return launch_pdl(distill_count_kernel, dim3(grid), dim3(256), 0, stream, 1, ids, values, B, K, V,
+                    static_cast<int8_t*>(nullptr), static_cast<unsigned int*>(nullptr), count) == cudaSuccess
              ? GH_OK
              : GH_ERR_CUDA;
 }
 
-gh_status_t distill_launch(const DistillArgs& a, gh_dtype_t dtype, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(tmin<int64_t>(a.B, 148 * 4));
-  ProfileScope prof(GH_KERNEL_DISTILL, stream);
+gh_status_t distill_launch(const DistillArgs& args, gh_dtype_t dtype, float* loss, cudaStream_t stream) {
+  DistillArgs a = args;
+  const int es = dtype == GH_F32 ? 4 : 2;
+  // Scratch: the counts, a flag per row, and the row losses unless the caller takes them.
+  const size_t flag_bytes = (static_cast<size_t>(a.B) + 15) / 16 * 16;
+  void* scratch = nullptr;
+  gh_status_t st = scratch_alloc(
+      &scratch, 4 * kCountParts + flag_bytes + (a.row_loss ? 0 : static_cast<size_t>(a.B) * sizeof(float)), stream);
+  if (st != GH_OK) return st;
+  char* p = static_cast<char*>(scratch);
+  a.parts = reinterpret_cast<unsigned int*>(p);
+  a.flags = reinterpret_cast<int8_t*>(p + 4 * kCountParts);
+  if (!a.row_loss) a.row_loss = reinterpret_cast<float*>(p + 4 * kCountParts + flag_bytes);
+  a.nparts = static_cast<int>(tmin<int64_t>((a.B + 7) / 8, kCountParts));
   note_launch();
-  const cudaError_t e =
-      dtype == GH_F32 ? launch_pdl(distill_kernel<float>, dim3(grid), dim3(kDistillThreads), 0, stream, 1, a)
-                      : launch_pdl(distill_kernel<uint16_t>, dim3(grid), dim3(kDistillThreads), 0, stream, 1, a);
-  return e == cudaSuccess ? GH_OK : GH_ERR_CUDA;
+  if (launch_pdl(distill_count_kernel, dim3(static_cast<unsigned>(a.nparts)), dim3(256), 0, stream, 1, a.ids, a.values,
+                 a.B, a.K, a.V, a.flags, a.parts, static_cast<unsigned long long*>(nullptr)) != cudaSuccess)
+    st = GH_ERR_CUDA;
+
+  // CTAs per row: enough that the rows in flight stay well inside L2 (a CTA's
+  // part at most 128 KiB), and for small batches that the SMs have work, down
+  // to 8 KiB a CTA.
+  const int64_t chunks = a.V * es / 16;
+  const int sms = token_sm_count();
+  int C = 1;
+  while (C < 8 && (chunks * 16 > C * int64_t(128 * 1024) ||
+                   (a.B * C * 2 <= 2 * sms && chunks * 16 >= 2 * C * int64_t(8 * 1024))))
+    C *= 2;
+  a.cluster = C;
+  a.slice_chunks = (chunks + C - 1) / C;
+  if (a.B * C > INT32_MAX) st = st == GH_OK ? GH_ERR_UNSUPPORTED : st;
+  if (st == GH_OK) {
+    ProfileScope prof(GH_KERNEL_DISTILL, stream);
+    note_launch();
+    const auto kern = es == 4 ? distill_kernel<float> : distill_kernel<uint16_t>;
+    if (launch_pdl(kern, dim3(static_cast<unsigned>(a.B * C)), dim3(kDistillThreads), 0, stream, C, a) != cudaSuccess)
+      st = GH_ERR_CUDA;
+  }
+  if (st == GH_OK) {
+    note_launch();
+    if (launch_pdl(distill_reduce_kernel, dim3(1), dim3(1024), 0, stream, 1, a, loss) != cudaSuccess) st = GH_ERR_CUDA;
+  }
+  scratch_free(scratch, stream);
+  return st;
 }
 
 }  // namespace gh
