@@ -10,12 +10,21 @@
 // whose value is -inf is none; a row without entries has no loss and a zero
 // gradient.
 //
-// distill_kernel: 15 streaming warps and one for the teacher's side per row, or a cluster of CTAs for long rows and
-// small batches.  The first pass sums 2^(x c - R) as the log-probabilities'
-// forward does; the second reads the row again, from L2 (the rows in flight,
-// two per SM, are far smaller), and stores the dense part scale T Q p_j; then
-// one warp, which has worked out the teacher's side meanwhile, stores the K
-// elements that differ.  HBM sees one read and one write of every logit.
+// distill_kernel: 7 streaming warps and one for the teacher's side per row, or
+// a cluster of such CTAs for long rows and small batches; three CTAs on an SM.
+// The first pass sums 2^(x c - R) as the log-probabilities' forward does; the
+// second reads the row again, from L2 (the rows in flight are a third of it),
+// and stores the dense part scale T Q p_j; then the last warp, which has worked
+// out the teacher's side and the loss meanwhile, stores the K elements that
+// differ.  HBM sees one read and one write of every logit.
+//
+// Bound by HBM and the row ends for fp32 ([4096, 50257], 32 entries: 317 us, 5.2
+// TB/s), by the two exponentials of an element for bf16 ([8192, 50257]: 344 us).
+// Warps x CTAs per SM on those two: 7 x 3 as taken, 7 x 4 371 / 327, 9 x 3 356 /
+// 320, 15 x 2 356 / 356, 11 x 2 352 / 342, 5 x 5 393 / 371.  Rows are split over
+// a cluster from 128 KiB on: at 256 KiB the rows in flight outgrow L2 (fp32 382
+// us, [1024, 262144] bf16 270 us against 241), at 64 KiB the exchanges cost more
+// (424 us for the bf16 rows at 7 x 4).
 #include "ce.h"
 #include "linear_ce.h"
 #include "profile.h"
@@ -26,7 +35,7 @@ namespace gh {
 
 namespace {
 
-constexpr int kDistillWarps = 15;  // that stream the row; one more has the teacher's side
+constexpr int kDistillWarps = 7;  // that stream the row; one more has the teacher's side
 constexpr int kDistillThreads = 32 * (kDistillWarps + 1);
 constexpr int kLaneEntries = GH_MAX_TOP_K / 32;
 constexpr int kCountParts = 64;  // CTAs of the counting kernel
@@ -167,6 +176,15 @@ __device__ __forceinline__ void dense_chunk(const uint4& q, float sub, float c, 
   }
 }
 
+// The streaming warps' gradient stores are done (they arrive, the last warp waits).
+constexpr int kStoredBarrier = 1;
+__device__ __forceinline__ void stored_arrive() {
+  asm volatile("barrier.cta.arrive %0, %1;" ::"n"(kStoredBarrier), "n"(kDistillThreads) : "memory");
+}
+__device__ __forceinline__ void stored_wait() {
+  asm volatile("barrier.cta.sync %0, %1;" ::"n"(kStoredBarrier), "n"(kDistillThreads) : "memory");
+}
+
 struct DistillShared {
   float2 state[kDistillWarps];  // the streaming warps' (reference, sum)
   float2 part;                  // this CTA's, read by the cluster's others
@@ -175,7 +193,7 @@ struct DistillShared {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(DistillArgs a) {
+__global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillArgs a) {
   constexpr int ES = Elem<T>::kBytes;
   __shared__ DistillShared sh;
   const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
@@ -210,6 +228,7 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(DistillArgs
   uint4 qa[kBatch], qb[kBatch];
   const int first = warp < kDistillWarps ? warp * kBatchChunks : nc;
   int c0 = first;
+  load(qa, c0);  // (before it is known whether the row counts)
   const bool counts = a.flags[row] != 0;
   int64_t e = -1;  // a ragged-end element, in lanes of the last warp
   constexpr int kEnds = kDistillWarps;
@@ -232,8 +251,7 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(DistillArgs
     return;
   }
 
-  // ---- first pass: the row's sum; the last warp also the teacher's side ----
-  load(qa, c0);
+  // ---- first pass: the row's sum; the last warp has the teacher's side ----
   Teacher t;
   float xk[kLaneEntries], edge = kNegInf, scale = 1.0f;
   if (warp == kEnds) {
@@ -287,41 +305,9 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(DistillArgs
     }
     if (warp == kEnds) {
       const RowDist d = row_dist<T>(st, r.src, a.V, a.c);
-      const float ct = scale * a.temperature;
       if (lane == 0) {
         sh.dist = d;
-        sh.coef = d.none ? kNaN : ct * t.total / d.s;
-      }
-      if (rank == 0) {
-        float loss = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kLaneEntries; ++i) {
-          const float lp = d.none ? kNaN : kLn2 * log2_p<T>(d, xk[i], a.c);
-          if (t.id[i] >= 0 && !(t.q[i] == 0.0f)) loss = fmaf(t.q[i], t.log_q[i] - lp, loss);
-        }
-        loss = warp_sum(loss);
-        if (lane == 0) a.row_loss[row] = a.temperature * a.temperature * loss;
-      }
-      if (with_grad) {
-        // the entries' elements: Q p less the q of every entry with this id
-        float qs[kLaneEntries];
-#pragma unroll
-        for (int i = 0; i < kLaneEntries; ++i) qs[i] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kLaneEntries; ++i) {
-          if (32 * i >= a.K) break;
-          for (int l = 0; l < tmin(32, a.K - 32 * i); ++l) {
-            const int id = __shfl_sync(0xffffffffu, t.id[i], l);
-            const float q = __shfl_sync(0xffffffffu, t.q[i], l);
-#pragma unroll
-            for (int j = 0; j < kLaneEntries; ++j) qs[j] += t.id[j] == id ? q : 0.0f;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kLaneEntries; ++i) {
-          const float p = d.none ? kNaN : ex2(fmaf(xk[i] - d.sub, a.c, -d.r)) / d.s;
-          xk[i] = ct * fmaf(t.total, p, -qs[i]);  // the gradient there
-        }
+        sh.coef = d.none ? kNaN : scale * a.temperature * t.total / d.s;
       }
     }
   }
@@ -333,40 +319,76 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(DistillArgs
     cluster_wait_acquire();
   }
 
-  // ---- second pass: the dense gradient, then the entries' elements ----
-  if (with_grad) {
-    const RowDist d = sh.dist;
-    const float coef = sh.coef;
-    auto put = [&](const uint4 (&q)[kBatch], int at) {
+  // ---- second pass: the streaming warps store the dense gradient; the last
+  // warp works out the loss and the entries' elements and stores those after them ----
+  const RowDist d = sh.dist;
+  const float coef = sh.coef;
+  if (warp == kEnds) {
+    if (rank == 0) {
+      float loss = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int c = at + i * kSegChunks + lane;
-        if (c >= nc) break;
-        uint8_t* p = gbase + 16 * static_cast<int64_t>(c);
-        if (d.sub == 0.0f) dense_chunk<T, false>(q[i], 0.0f, a.c, d.r, coef, p, congruent);
-        else dense_chunk<T, true>(q[i], d.sub, a.c, d.r, coef, p, congruent);
+      for (int i = 0; i < kLaneEntries; ++i) {
+        const float lp = d.none ? kNaN : kLn2 * log2_p<T>(d, xk[i], a.c);
+        if (t.id[i] >= 0 && !(t.q[i] == 0.0f)) loss = fmaf(t.q[i], t.log_q[i] - lp, loss);
       }
-    };
-    while (c0 < nc) {
-      if (c0 + kStep < nc) load(qb, c0 + kStep);
-      put(qa, c0);
-      c0 += kStep;
-      if (c0 >= nc) break;
-      if (c0 + kStep < nc) load(qa, c0 + kStep);
-      put(qb, c0);
-      c0 += kStep;
+      loss = warp_sum(loss);
+      if (lane == 0) a.row_loss[row] = a.temperature * a.temperature * loss;
+    }
+    if (!with_grad) return;
+    // Q p less the q of every entry with this id
+    float qs[kLaneEntries];
+#pragma unroll
+    for (int i = 0; i < kLaneEntries; ++i) qs[i] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kLaneEntries; ++i) {
+      if (32 * i >= a.K) break;
+      for (int l = 0; l < tmin(32, a.K - 32 * i); ++l) {
+        const int id = __shfl_sync(0xffffffffu, t.id[i], l);
+        const float q = __shfl_sync(0xffffffffu, t.q[i], l);
+#pragma unroll
+        for (int j = 0; j < kLaneEntries; ++j) qs[j] += t.id[j] == id ? q : 0.0f;
+      }
+    }
+    const float ct = scale * a.temperature;
+#pragma unroll
+    for (int i = 0; i < kLaneEntries; ++i) {
+      const float p = d.none ? kNaN : ex2(fmaf(xk[i] - d.sub, a.c, -d.r)) / d.s;
+      xk[i] = ct * fmaf(t.total, p, -qs[i]);  // the gradient there
     }
     if (e >= 0) Elem<T>::store(dst + e * ES, coef * ex2(fmaf(edge - d.sub, a.c, -d.r)));
-    __syncthreads();
-    if (warp == kEnds) {
-      // entries of this CTA's part of the row (in-place: their logits were read above)
-      const int64_t lo = rank == 0 ? 0 : (16 * from - r.lead) / ES;
-      const int64_t hi = rank == C - 1 ? a.V : (16 * (from + nc) - r.lead) / ES;
+    stored_wait();
+    // entries of this CTA's part of the row (in place, their logits were read above)
+    const int64_t lo = rank == 0 ? 0 : (16 * from - r.lead) / ES;
+    const int64_t hi = rank == C - 1 ? a.V : (16 * (from + nc) - r.lead) / ES;
 #pragma unroll
-      for (int i = 0; i < kLaneEntries; ++i)
-        if (t.id[i] >= 0 && t.id[i] >= lo && t.id[i] < hi) Elem<T>::store(dst + static_cast<int64_t>(t.id[i]) * ES, xk[i]);
-    }
+    for (int i = 0; i < kLaneEntries; ++i)
+      if (t.id[i] >= 0 && t.id[i] >= lo && t.id[i] < hi) Elem<T>::store(dst + static_cast<int64_t>(t.id[i]) * ES, xk[i]);
+    return;
   }
+  if (!with_grad) return;
+  auto put = [&](const uint4 (&q)[kBatch], int at) {
+    uint8_t* const p = gbase + 16 * static_cast<int64_t>(at + lane);
+    if (at + kBatchChunks <= nc && d.sub == 0.0f) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        dense_chunk<T, false>(q[i], 0.0f, a.c, d.r, coef, p + 16 * kSegChunks * i, congruent);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (at + i * kSegChunks + lane < nc)
+          dense_chunk<T, true>(q[i], d.sub, a.c, d.r, coef, p + 16 * kSegChunks * i, congruent);
+    }
+  };
+  while (c0 < nc) {
+    if (c0 + kStep < nc) load(qb, c0 + kStep);
+    put(qa, c0);
+    c0 += kStep;
+    if (c0 >= nc) break;
+    if (c0 + kStep < nc) load(qa, c0 + kStep);
+    put(qb, c0);
+    c0 += kStep;
+  }
+  stored_arrive();
 }
 
 // Sum of the row losses in a fixed order, in double, and the mean's division.
