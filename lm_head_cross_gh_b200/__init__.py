@@ -162,6 +162,9 @@ def _check(status: int, where: str) -> None:
 def _stream_handle(stream) -> int:
     import torch
     if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:  # the handle alone: building a Stream object takes longer than a small kernel's launch
+            return raw(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 

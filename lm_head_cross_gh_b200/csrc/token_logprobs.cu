@@ -11,16 +11,15 @@
 // ascending); the temperature does not change their order.
 //
 // The forward (logprobs_kernel) reads every logit once.  A row is cut into
-// segments of 512 bytes, one 16-byte load of a warp each; the warp that sums a
-// segment keeps the key of its largest logit in shared memory.  The k largest
-// logits lie in the k segments that come first by (largest logit descending,
-// position ascending): any other segment's logits have k segment maxima before
-// them.  So the alternatives cost one warp maximum per segment during the
+// segments (512 bytes, one 16-byte load of a warp; finer ones for short rows),
+// and the key of each segment's largest logit is kept in shared memory.  The k
+// largest logits lie in the k segments that come first by (largest logit
+// descending, position ascending): any other segment's logits have k segment
+// maxima before them.  So the alternatives cost a maximum per segment during the
 // pass, a selection among V / 256 (bf16) keys, and k segments read again from L2.
 #include <algorithm>
 #include <cstring>
 
-#include "linear_ce.h"
 #include "profile.h"
 #include "token_device.cuh"
 #include "token_ops.h"
@@ -30,10 +29,12 @@ namespace gh {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Forward.  One CTA of four warps per unit (a row, or a slice of one), seven or
-// eight of them on an SM, so that one's end (merge, alternatives) overlaps the
-// others' streams.  The warps take batches of four segments in turn, the next
-// batch's loads in flight while one is summed.
+// Forward.  One CTA of four warps per row, seven or eight of them on an SM, so
+// that one's end (merge, alternatives) overlaps the others' streams.  The warps
+// take batches of four segments in turn, the next batch's loads in flight while
+// one is summed.  Small batches and very long rows take a cluster of up to eight
+// CTAs per row, whose first merges the others' sums and alternatives through
+// distributed shared memory.
 //
 // Bound by HBM for fp32 logits ([4096, 50257]: 128 us, 6.4 TB/s), by the
 // exponentials and the instructions around them for bf16 ([8192, 50257]: 150
@@ -46,11 +47,19 @@ namespace {
 
 constexpr int kLpWarps = 4;
 constexpr int kLpThreads = 32 * kLpWarps;
-constexpr int kLpMaxSegs = 2048;  // segments of a unit whose keys are kept (8 KiB)
-constexpr int kCandidates = 512;  // logits of the picked segments that reach the threshold, before the slow way
+constexpr int kMaxSlices = 8;       // CTAs per row: a portable cluster
+constexpr int kLpMaxSegs = 16384;   // 512-byte segments of a CTA whose keys are kept (64 KiB)
+constexpr int kCandidates = 512;    // logits of the picked segments that reach the threshold, before the slow way
+
+// Segments: a warp's load, a quarter of four lanes' loads, one lane's, or one
+// logit.  The finest are for rows with few segments per alternative.
+enum SegKind : int { kSegElement = 0, kSegChunk = 1, kSegQuad = 2, kSegWarp = 3 };
+// What a kernel keeps for alternatives: nothing, warp segments' keys, or finer ones'.
+enum TopMode : int { kTopNone = 0, kTopWarp = 1, kTopFine = 2 };
 
 struct LpShared {
   float4 state[kLpWarps];  // the warps' (reference, sum, weighted sum)
+  float4 part;             // this CTA's, read by the cluster's first
   RowDist dist;
   int count, listed;
   float least;
@@ -58,34 +67,15 @@ struct LpShared {
 };
 struct LpTopShared {
   uint64_t buf[kCandidates];
-  uint64_t out[GH_MAX_TOP_K];
+  uint64_t out[GH_MAX_TOP_K];  // this CTA's alternatives, largest first, zeros behind them
 };
 static_assert(kCandidates >= kTopBuf, "the slow way's buffer");
-
-// Where unit u lies: row, slice, and its chunks of the row.
-struct Unit {
-  int64_t row;
-  int slice;
-  int64_t c0, c1;  // chunks [c0, c1) of the row
-};
-
-__device__ __forceinline__ int64_t unit_row(const StatArgs& a, int64_t u) { return a.slices == 1 ? u : u / a.slices; }
-
-__device__ __forceinline__ Unit unit_of(const StatArgs& a, int64_t u, int64_t row, const RowGeo& r) {
-  Unit w;
-  w.row = row;
-  w.slice = static_cast<int>(u - row * a.slices);
-  const int64_t per = static_cast<int64_t>(a.slice_segs) * kSegChunks;
-  w.c0 = tmin(r.c_hi, r.c_lo + w.slice * per);
-  w.c1 = w.slice == a.slices - 1 ? r.c_hi : tmin(r.c_hi, w.c0 + per);
-  return w;
-}
+static_assert(kMaxSlices * GH_MAX_TOP_K <= 1024, "the keys gathered by a cluster's first CTA");
 
 // Rows that count: 1; ignored: 0; an index outside [0, V): -1.
-__device__ __forceinline__ int row_kind(const StatArgs& a, int64_t row) {
-  if (a.flags) return a.flags[row];
-  const int64_t t = a.lp.index[row];
-  if (t == a.lp.ignore_index) return 0;
+__device__ __forceinline__ int row_kind(const LogprobArgs& a, int64_t row) {
+  const int64_t t = a.index[row];
+  if (t == a.ignore_index) return 0;
   return t >= 0 && t < a.V ? 1 : -1;
 }
 
@@ -118,7 +108,7 @@ __device__ __forceinline__ void write_values(const LogprobArgs& o, int64_t row, 
   o.lse[row] = d.none ? kNaN : dist_lse(d, o.temperature);
 }
 
-// The k-th largest of keys[] (n4 groups of four, zeros as padding), found bit by
+// The k-th largest of keys[] (n4 groups of four; zeros as padding), found bit by
 // bit, by one warp; stops at a prefix that exactly k keys reach (*exact).  bf16
 // keys differ in their upper 16 bits only.  R > 0: up to 32 R groups, kept in
 // registers.
@@ -219,30 +209,50 @@ __device__ __forceinline__ uint32_t reach_mask(const uint4& q, float least) {
   return m;
 }
 
-// The k largest keys of the listed segments and the ragged ends, by one warp
-// and whatever their number (ties can make it large): out[] and the count.
-template <typename T>
-__device__ __noinline__ int pick_slowly(LpTopShared& tsh, const RowGeo& r, const Unit& w, const int* list, int n, int k,
-                                        float edge, int64_t e) {
-  constexpr int ES = Elem<T>::kBytes, EPC = 16 / ES;
+__device__ __forceinline__ uint64_t ld_dsmem_u64(uint32_t addr) {
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// A CTA's part of a row: its first chunk, how many, that chunk's first element's
+// index in the row, and the chunks of a segment (2^shift).
+struct RowPart {
+  const uint4* chunks;
+  int64_t j0;
+  int nc, shift;
+};
+
+// Loads, by one warp, the chunks of the 32 >> shift listed segments from place
+// `at` on: a lane's chunk of the part (nc: none).
+__device__ __forceinline__ int listed_chunk(RowPart w, const int* list, int n, int at) {
   const int lane = static_cast<int>(threadIdx.x) & 31;
-  WarpTopK top{tsh.buf, tsh.out, k, 0, 0};
-  for (int i = 0; i < n; ++i) {
-    const int64_t c = w.c0 + static_cast<int64_t>(list[i]) * kSegChunks + lane;
-    const uint4 q = c < w.c1 ? __ldcg(reinterpret_cast<const uint4*>(r.base + 16 * c)) : make_uint4(0, 0, 0, 0);
+  at += lane >> w.shift;
+  return at < n ? (list[at] << w.shift) + (lane & ((1 << w.shift) - 1)) : w.nc;
+}
+
+// The k largest keys of the listed segments and the ragged ends, by one warp
+// and whatever their number (ties can make it large): into out[]; returns how many.
+template <typename T>
+__device__ __noinline__ int pick_slowly(uint64_t* buf, uint64_t* out, RowPart w, const int* list, int n, int k,
+                                        float edge, int64_t e) {
+  constexpr int EPC = 16 / Elem<T>::kBytes;
+  WarpTopK top{buf, out, k, 0, 0};
+  for (int at = 0; at < n; at += 32 >> w.shift) {
+    const int c = listed_chunk(w, list, n, at);
+    const uint4 q = c < w.nc ? __ldcg(w.chunks + c) : make_uint4(0, 0, 0, 0);
     float v[EPC];
     unpack16<T>(q, v);
-    const int64_t j0 = (16 * c - r.lead) / ES;
 #pragma unroll
-    for (int j = 0; j < EPC; ++j) top.push(rank_key(order_key(v[j]), j0 + j), c < w.c1);
+    for (int j = 0; j < EPC; ++j) top.push(rank_key(order_key(v[j]), w.j0 + static_cast<int64_t>(c) * EPC + j), c < w.nc);
   }
   top.push(rank_key(order_key(edge), e), e >= 0);
   top.cut();
   return top.n;
 }
 
-template <typename T, bool ENT, bool TOPK>
-__global__ void __launch_bounds__(kLpThreads, TOPK ? 7 : 8) logprobs_kernel(StatArgs a) {
+template <typename T, int TOP, bool SPLIT>
+__global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_kernel(LogprobArgs a) {
   constexpr int ES = Elem<T>::kBytes, EPC = 16 / ES;
   __shared__ LpShared sh;
   __shared__ LpTopShared tsh;
@@ -251,14 +261,15 @@ __global__ void __launch_bounds__(kLpThreads, TOPK ? 7 : 8) logprobs_kernel(Stat
   const int tid = static_cast<int>(threadIdx.x);
   pdl_wait();
   pdl_trigger();
-  const int64_t u = blockIdx.x;
-  const int64_t row = unit_row(a, u);
+  const int rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
+  const int64_t row = SPLIT ? blockIdx.x / a.slices : blockIdx.x;
+  const bool last = !SPLIT || rank == a.slices - 1;
   const RowGeo r = row_geo<ES>(a.logits, row, a.ld, a.V);
-  const Unit w = unit_of(a, u, row, r);
-  const int nc = static_cast<int>(w.c1 - w.c0);
-  const uint4* const chunks = reinterpret_cast<const uint4*>(r.base) + w.c0 + lane;
+  const int64_t from = SPLIT ? tmin(r.c_hi, r.c_lo + rank * a.slice_chunks) : r.c_lo;
+  const int nc = static_cast<int>((last ? r.c_hi : tmin(r.c_hi, from + a.slice_chunks)) - from);
+  const uint4* const chunks = reinterpret_cast<const uint4*>(r.base) + from + lane;
   const uint32_t none = ES == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
-  auto load = [&](uint4 (&q)[kBatch], int c0) {  // c0: the batch's first chunk of the unit
+  auto load = [&](uint4 (&q)[kBatch], int c0) {  // c0: the batch's first chunk of the part
     if (c0 + kBatchChunks <= nc) {
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) q[i] = __ldcg(chunks + c0 + i * kSegChunks);
@@ -275,8 +286,8 @@ __global__ void __launch_bounds__(kLpThreads, TOPK ? 7 : 8) logprobs_kernel(Stat
   int c0 = warp * kBatchChunks;
   load(qa, c0);
   const int kind = row_kind(a, row);
-  if (kind <= 0) {
-    if (!a.part && warp == 0) write_no_row(a.lp, row, kind);
+  if (kind <= 0) {  // (the same in every CTA of a cluster)
+    if (rank == 0 && warp == 0) write_no_row(a, row, kind);
     return;
   }
   // the last warp takes the ragged ends, and with them the row's values
@@ -285,19 +296,40 @@ __global__ void __launch_bounds__(kLpThreads, TOPK ? 7 : 8) logprobs_kernel(Stat
   float edge = kNegInf, xt = 0.0f;
   if (warp == kEnds) {
     e = edge_element(r, a.V, lane);
-    if (lane < 16 ? w.slice != 0 : w.slice != a.slices - 1) e = -1;
+    if (lane < 16 ? rank != 0 : !last) e = -1;
     if (e >= 0) edge = Elem<T>::load(r.src + e * ES);
-    if (!a.part) xt = Elem<T>::load(r.src + a.lp.index[row] * ES);
+    if (rank == 0) xt = Elem<T>::load(r.src + a.index[row] * ES);
   }
 
   WarpSums sums{kNegInf, kNegInf, {}, {}};
   auto fold = [&](const uint4 (&q)[kBatch], int c0) {
     float m[kBatch];
-    fold_batch<T, ENT, TOPK>(sums, q, a.c, a.low, m);
-    if constexpr (TOPK) {
+    fold_batch<T, true, TOP == kTopWarp>(sums, q, a.c, a.low, m);
+    if constexpr (TOP == kTopWarp) {
       static_assert(kBatch == 4, "one lane stores each segment's key");
       const float mine = lane == 0 ? m[0] : lane == 1 ? m[1] : lane == 2 ? m[2] : m[3];
       if (lane < kBatch) seg_keys[c0 / kSegChunks + lane] = order_key(mine);
+    }
+    if constexpr (TOP == kTopFine) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int c = c0 + i * kSegChunks + lane;
+        if (a.seg_kind == kSegElement) {
+          float v[EPC];
+          unpack16<T>(q[i], v);
+#pragma unroll
+          for (int j = 0; j < EPC; ++j) seg_keys[c * EPC + j] = order_key(v[j]);
+          continue;
+        }
+        float v = max_of4<T>(q[i]);
+        if (a.seg_kind == kSegQuad) {
+          v = f32_max_nan(v, __shfl_xor_sync(0xffffffffu, v, 1));
+          v = f32_max_nan(v, __shfl_xor_sync(0xffffffffu, v, 2));
+          if ((lane & 3) == 0) seg_keys[c >> 2] = order_key(v);
+        } else {
+          seg_keys[c] = order_key(v);
+        }
+      }
     }
   };
   constexpr int kStep = kLpWarps * kBatchChunks;
@@ -310,19 +342,26 @@ __global__ void __launch_bounds__(kLpThreads, TOPK ? 7 : 8) logprobs_kernel(Stat
     fold(qb, c0);
     c0 += kStep;
   }
-  const float2 sa = __fadd2_rn(sums.s[0], sums.s[1]), ta = __fadd2_rn(sums.t[0], sums.t[1]);
-  SoftState st{sums.r, sa.x + sa.y, ta.x + ta.y};
+  {
+    const float2 sa = __fadd2_rn(sums.s[0], sums.s[1]), ta = __fadd2_rn(sums.t[0], sums.t[1]);
+    SoftState st{sums.r, sa.x + sa.y, ta.x + ta.y};
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    st.s += __shfl_xor_sync(0xffffffffu, st.s, o);
-    if (ENT) st.t += __shfl_xor_sync(0xffffffffu, st.t, o);
+    for (int o = 16; o > 0; o >>= 1) {
+      st.s += __shfl_xor_sync(0xffffffffu, st.s, o);
+      st.t += __shfl_xor_sync(0xffffffffu, st.t, o);
+    }
+    if (warp == kEnds) st = combine(st, warp_combine(state_of_element(edge, a.c)));
+    if (lane == 0) sh.state[warp] = make_float4(st.r, st.s, st.t, 0.0f);
+    if (TOP != kTopNone && tid == 0) sh.count = 0;
   }
-  if (warp == kEnds) st = combine(st, warp_combine(state_of_element(edge, a.c)));
-  if (lane == 0) sh.state[warp] = make_float4(st.r, st.s, st.t, 0.0f);
-  if (TOPK && tid == 0) sh.count = 0;
   __syncthreads();
-  const int segs = (nc + kSegChunks - 1) / kSegChunks;
-  if (TOPK && warp == 0) {
+
+  // the last warp merges the sums while warp 0 picks the segments
+  const RowPart part{chunks - lane, (16 * from - r.lead) / ES, nc,
+                     TOP == kTopWarp || a.seg_kind == kSegWarp ? 5 : a.seg_kind == kSegQuad ? 2 : 0};
+  const bool elements = TOP == kTopFine && a.seg_kind == kSegElement;
+  if (TOP != kTopNone && warp == 0) {
+    const int segs = elements ? nc * EPC : (nc + (1 << part.shift) - 1) >> part.shift;
     // keys to a multiple of 128 (the last batch's are there already)
     for (int j = segs + lane; j < (segs + 127) / 128 * 128; j += 32) seg_keys[j] = 0;
     __syncwarp();
@@ -340,122 +379,141 @@ __global__ void __launch_bounds__(kLpThreads, TOPK ? 7 : 8) logprobs_kernel(Stat
       const float4 v = sh.state[i];
       all = combine(all, SoftState{v.x, v.y, v.z});
     }
-    if (a.part) {
-      if (lane == 0) a.part[u] = make_float4(all.r, all.s, all.t, 0.0f);
+    if (SPLIT) {
+      if (lane == 0) sh.part = make_float4(all.r, all.s, all.t, 0.0f);
     } else {
       const RowDist d = row_dist<T>(all, r.src, a.V, a.c);
       if (lane == 0) {
-        write_values<T>(a.lp, row, d, xt);
-        if (TOPK) sh.dist = d;
+        write_values<T>(a, row, d, xt);
+        if (TOP != kTopNone) sh.dist = d;
       }
     }
   }
-  if constexpr (TOPK) {
+  int n = 0;
+  if constexpr (TOP != kTopNone) {
     __syncthreads();
+    // every logit of the picked segments that reaches the threshold is a candidate
     const int listed = sh.listed;
     const float least = sh.least;
     auto offer = [&](float x, int64_t j) {
       const int p = atomicAdd(&sh.count, 1);
       if (p < kCandidates) tsh.buf[p] = rank_key(order_key(x), j);
     };
-    constexpr int kAhead = 4;
-    for (int i0 = warp; i0 < listed; i0 += kLpWarps * kAhead) {
-      uint4 q[kAhead];
-      int c[kAhead];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int at = i0 + i * kLpWarps;
-        c[i] = at < listed ? sh.list[at] * kSegChunks + lane : nc;
-        if (c[i] < nc) q[i] = __ldcg(chunks - lane + c[i]);
+    if (elements) {
+      for (int i = tid; i < listed; i += kLpThreads) {
+        const int at = sh.list[i];
+        offer(key_value(static_cast<uint64_t>(seg_keys[at]) << 32), part.j0 + at);
       }
+    } else {
+      constexpr int kAhead = 4;
+      const int per = 32 >> part.shift;  // segments of a warp's load
+      for (int i0 = warp * per; i0 < listed; i0 += kLpWarps * kAhead * per) {
+        uint4 q[kAhead];
+        int c[kAhead];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (c[i] >= nc) continue;
-        uint32_t hits = reach_mask<T>(q[i], least);
-        if (hits == 0) continue;
-        float v[EPC];
-        unpack16<T>(q[i], v);
-        const int64_t j0 = (16 * (w.c0 + c[i]) - r.lead) / ES;
-        while (hits) {
-          const int j = __ffs(hits) - 1;
-          hits &= hits - 1;
-          float x = v[0];
+        for (int i = 0; i < kAhead; ++i) {
+          c[i] = listed_chunk(part, sh.list, listed, i0 + i * kLpWarps * per);
+          if (c[i] < nc) q[i] = __ldcg(part.chunks + c[i]);
+        }
 #pragma unroll
-          for (int k = 1; k < EPC; ++k) x = j == k ? v[k] : x;
-          offer(x, j0 + j);
+        for (int i = 0; i < kAhead; ++i) {
+          if (c[i] >= nc) continue;
+          uint32_t hits = reach_mask<T>(q[i], least);
+          if (hits == 0) continue;
+          float v[EPC];
+          unpack16<T>(q[i], v);
+          const int64_t j0 = part.j0 + static_cast<int64_t>(c[i]) * EPC;
+          while (hits) {
+            const int j = __ffs(hits) - 1;
+            hits &= hits - 1;
+            float x = v[0];
+#pragma unroll
+            for (int k = 1; k < EPC; ++k) x = j == k ? v[k] : x;
+            offer(x, j0 + j);
+          }
         }
       }
     }
     if (e >= 0 && edge >= least) offer(edge, e);
     __syncthreads();
-    int n = sh.count;
+    n = sh.count;
     if (n > kCandidates) {  // the same n in every thread
       __syncthreads();
       if (warp == kEnds) {
-        n = pick_slowly<T>(tsh, r, w, sh.list, listed, a.top_k, edge, e);
+        n = pick_slowly<T>(tsh.buf, tsh.out, part, sh.list, listed, a.top_k, edge, e);
         if (lane == 0) sh.count = n;
       }
       __syncthreads();
       n = sh.count;
     }
-    // each key's place is the number of larger keys (keys are distinct, so
-    // the order of the offers does not matter)
+    // Each candidate's place is the number of larger ones (keys are distinct, so
+    // the order of the offers does not matter).  A part, or a row without a
+    // distribution, may have fewer than top_k.
     const RowDist d = sh.dist;
+    auto put = [&](int place, uint64_t key) {
+      if (SPLIT) tsh.out[place] = key;
+      else write_top<T>(a, row, d, place, key);
+    };
     for (int i = tid; i < n; i += kLpThreads) {
       const uint64_t key = tsh.buf[i];
       int above = 0;
       for (int j = 0; j < n; ++j) above += tsh.buf[j] > key ? 1 : 0;
-      if (above >= a.top_k) continue;
-      if (a.part) a.part_keys[u * a.top_k + above] = key;
-      else write_top<T>(a.lp, row, d, above, key);
+      if (above < a.top_k) put(above, key);
     }
-    // a slice, or a row without a distribution, may have fewer
-    for (int i = tmin(n, a.top_k) + tid; i < a.top_k; i += kLpThreads) {
-      if (a.part) a.part_keys[u * a.top_k + i] = 0;
-      else write_top<T>(a.lp, row, d, i, 0);
-    }
+    for (int i = tmin(n, a.top_k) + tid; i < a.top_k; i += kLpThreads) put(i, 0);
   }
-}
-
-// Rows in slices: one warp per row merges the slices' states and alternatives.
-constexpr int kMergeWarps = 4;
-
-template <typename T>
-__global__ void __launch_bounds__(32 * kMergeWarps) logprobs_merge_kernel(StatArgs a) {
-  constexpr int ES = Elem<T>::kBytes;
-  __shared__ uint64_t buf[kMergeWarps][kTopBuf], out[kMergeWarps][GH_MAX_TOP_K];
-  pdl_wait();
-  pdl_trigger();
-  const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeWarps + warp; row < a.B;
-       row += static_cast<int64_t>(gridDim.x) * kMergeWarps) {
-    const int kind = row_kind(a, row);
-    if (kind <= 0) {
-      write_no_row(a.lp, row, kind);
-      continue;
-    }
-    const uint8_t* src = static_cast<const uint8_t*>(a.logits) + row * a.ld * ES;
-    const float xt = Elem<T>::load(src + a.lp.index[row] * ES);
-    SoftState st{kNegInf, 0.0f, 0.0f};
-    for (int i = lane; i < a.slices; i += 32) {
-      const float4 v = a.part[row * a.slices + i];
-      st = combine(st, SoftState{v.x, v.y, v.z});
-    }
-    st = warp_combine(st);
-    WarpTopK top{buf[warp], out[warp], a.top_k, 0, 0};
-    if (a.top_k > 0) {
-      const uint64_t* keys = a.part_keys + row * a.slices * a.top_k;
-      const int n = a.slices * a.top_k;
-      for (int i = 0; i < n; i += 32) {
-        const uint64_t key = i + lane < n ? keys[i + lane] : 0;
-        top.push(key, key != 0);
-      }
-      top.cut();
-    }
-    const RowDist d = row_dist<T>(st, src, a.V, a.c);
-    if (lane == 0) write_values<T>(a.lp, row, d, xt);
-    for (int k = lane; k < a.top_k; k += 32) write_top<T>(a.lp, row, d, k, k < top.n ? top.out[k] : 0);
+  if constexpr (SPLIT) {
+    // the cluster's first CTA merges the parts
     __syncwarp();
+    cluster_arrive_release();
+    cluster_wait_acquire();
+    if (rank == 0) {
+      if (warp == kEnds) {
+        SoftState all{kNegInf, 0.0f, 0.0f};
+        for (int i = 0; i < a.slices; ++i) {
+          const uint32_t p = map_to_rank(&sh.part, i);
+          all = combine(all, SoftState{ld_dsmem_f32(p), ld_dsmem_f32(p + 4), ld_dsmem_f32(p + 8)});
+        }
+        const RowDist d = row_dist<T>(all, r.src, a.V, a.c);
+        if (lane == 0) {
+          write_values<T>(a, row, d, xt);
+          sh.dist = d;
+        }
+      }
+      if constexpr (TOP != kTopNone) {
+        // the parts' alternatives in the row's order, then as logits of a row
+        // whose segments are single logits
+        const int total = a.slices * a.top_k;
+        uint64_t* const gathered = reinterpret_cast<uint64_t*>(seg_keys + (total + 127) / 128 * 128);
+        for (int i = tid; i < (total + 127) / 128 * 128; i += kLpThreads) {
+          uint64_t key = 0;
+          if (i < total) {
+            key = ld_dsmem_u64(map_to_rank(&tsh.out[i % a.top_k], i / a.top_k));
+            gathered[i] = key;
+          }
+          seg_keys[i] = static_cast<uint32_t>(key >> 32);
+        }
+        __syncthreads();
+        if (warp == 0) {
+          uint32_t thr;
+          const int got = pick_segments<T>(seg_keys, total, a.top_k, sh.list, &thr);
+          if (lane == 0) sh.listed = got;
+        }
+        __syncthreads();
+        const RowDist d = sh.dist;
+        const int got = sh.listed;
+        for (int i = tid; i < got; i += kLpThreads) {
+          const uint64_t key = gathered[sh.list[i]];
+          int above = 0;
+          for (int j = 0; j < got; ++j) above += gathered[sh.list[j]] > key ? 1 : 0;
+          write_top<T>(a, row, d, above, key);
+        }
+      }
+    }
+    // no CTA leaves before its part has been read
+    __syncwarp();
+    cluster_arrive_release();
+    cluster_wait_acquire();
   }
 }
 
@@ -616,32 +674,6 @@ int token_sm_count() {
   return n > 0 ? n : 148;
 }
 
-// Slices per row.  CTAs of a wave share the SMs; a unit costs its segments
-// plus about 24 (a unit's fixed work), the merge about 200 (2.5 us).  With
-// alternatives a unit has at most kLpMaxSegs segments.
-int plan_slices(int64_t B, int64_t segs, bool topk, int64_t resident) {
-  const int64_t lo = topk ? tmax<int64_t>(1, (segs + kLpMaxSegs - 1) / kLpMaxSegs) : 1;
-  const int64_t hi = tmax<int64_t>(lo, tmin<int64_t>(64, segs / kBatch));
-  int64_t best = lo, cost = INT64_MAX;
-  for (int64_t s = lo; s <= hi; ++s) {
-    const int64_t c = ((B * s + resident - 1) / resident) * ((segs + s - 1) / s + 24) + (s > 1 ? 200 : 0);
-    if (c < cost) {
-      cost = c;
-      best = s;
-    }
-    if (B >= 8 * resident) break;
-  }
-  return static_cast<int>(best);
-}
-
-using StatKernel = void (*)(StatArgs);
-
-template <bool ENT, bool TOPK>
-StatKernel stat_kernel(int es) {
-  return es == 4 ? static_cast<StatKernel>(logprobs_kernel<float, ENT, TOPK>)
-                 : static_cast<StatKernel>(logprobs_kernel<uint16_t, ENT, TOPK>);
-}
-
 // The lowest logit that keeps x c finite, as packed bf16 or fp32 bits.
 uint32_t low_bits(float c, int es) {
   const float low = -std::min(3.3e38f, 3.3e38f / c);
@@ -650,53 +682,58 @@ uint32_t low_bits(float c, int es) {
   return es == 4 ? b : (b >> 16) * 0x10001u;  // truncated towards 0
 }
 
+using LogprobKernel = void (*)(LogprobArgs);
+
+template <typename T>
+LogprobKernel logprobs_kernel_for(int top, bool split) {
+  if (top == kTopNone) return split ? logprobs_kernel<T, kTopNone, true> : logprobs_kernel<T, kTopNone, false>;
+  if (top == kTopWarp) return split ? logprobs_kernel<T, kTopWarp, true> : logprobs_kernel<T, kTopWarp, false>;
+  return split ? logprobs_kernel<T, kTopFine, true> : logprobs_kernel<T, kTopFine, false>;
+}
+
 }  // namespace
 
-gh_status_t logprobs_launch(const LogprobArgs& o, gh_dtype_t dtype, cudaStream_t stream) {
-  const int es = dtype == GH_F32 ? 4 : 2;
-  const bool topk = o.top_k > 0;
+gh_status_t logprobs_launch(const LogprobArgs& args, gh_dtype_t dtype, cudaStream_t stream) {
+  LogprobArgs a = args;
+  const int es = dtype == GH_F32 ? 4 : 2, epc = 16 / es, k = a.top_k;
   const int sms = token_sm_count();
-  StatArgs a{};
-  a.logits = o.logits;
-  a.B = o.B;
-  a.V = o.V;
-  a.ld = o.ld;
-  a.c = o.c;
-  a.low = low_bits(o.c, es);
-  a.top_k = o.top_k;
-  a.lp = o;
-  constexpr int kResident = 8;  // CTAs of an SM
-  const int64_t segs = (o.V * es / 16 + kSegChunks - 1) / kSegChunks;
-  a.slices = plan_slices(o.B, segs, topk, static_cast<int64_t>(sms) * kResident);
-  a.slice_segs = static_cast<int>(tmax<int64_t>(1, (segs + a.slices - 1) / a.slices));
-  const int64_t units = o.B * a.slices;
-  if (units > INT32_MAX) return GH_ERR_UNSUPPORTED;  // one CTA each
+  const int64_t chunks = a.V * es / 16;
+  a.low = low_bits(a.c, es);
+  // CTAs per row: as many as are resident together, each with at least one
+  // batch a warp; for alternatives, at most kLpMaxSegs segments each.
+  constexpr int kResident = 7;
+  int S = 1;
+  while (S < kMaxSlices &&
+         ((a.B * S * 2 <= static_cast<int64_t>(sms) * kResident && chunks >= int64_t(2) * S * kLpWarps * kBatchChunks) ||
+          (k > 0 && chunks > int64_t(S) * kLpMaxSegs * kSegChunks)))
+    S *= 2;
+  a.slices = S;
+  a.slice_chunks = (chunks + S - 1) / S;
+  if (a.B * S > INT32_MAX || (k > 0 && a.slice_chunks > int64_t(kLpMaxSegs) * kSegChunks)) return GH_ERR_UNSUPPORTED;
 
-  void* scratch = nullptr;
-  if (a.slices > 1) {
-    const gh_status_t st = scratch_alloc(&scratch, static_cast<size_t>(units) * (16 + 8 * o.top_k), stream);
-    if (st != GH_OK) return st;
-    a.part = static_cast<float4*>(scratch);
-    a.part_keys = reinterpret_cast<uint64_t*>(static_cast<char*>(scratch) + units * 16);
+  // Segments: the largest kind with three per alternative (then about k of them
+  // hold the alternatives and little else reaches their threshold); single logits
+  // where even chunks are fewer than two per alternative.
+  int top = kTopNone, smem = 0;
+  if (k > 0) {
+    const int64_t n = a.slice_chunks;
+    a.seg_kind = n >= int64_t(3) * k * 32 ? kSegWarp : n >= int64_t(3) * k * 4 ? kSegQuad : n >= int64_t(2) * k ? kSegChunk : kSegElement;
+    top = a.seg_kind == kSegWarp ? kTopWarp : kTopFine;
+    const int64_t whole = (n + kBatchChunks - 1) / kBatchChunks * kBatchChunks;  // whole batches are stored
+    const int64_t keys = a.seg_kind == kSegWarp   ? whole / 32
+                         : a.seg_kind == kSegQuad ? whole / 4
+                         : a.seg_kind == kSegChunk ? whole
+                                                   : whole * epc;
+    smem = static_cast<int>((keys + 127) / 128 * 128 * 4);
+    if (S > 1) smem = tmax(smem, (S * k + 127) / 128 * 128 * 4 + S * k * 8);  // keys, and keys with positions
   }
-  const StatKernel kern = topk ? stat_kernel<true, true>(es) : stat_kernel<true, false>(es);
-  const int smem = topk ? (a.slice_segs + 127) / 128 * 128 * 4 : 0;
-  gh_status_t st = GH_OK;
-  {
-    ProfileScope prof(GH_KERNEL_LOGPROBS, stream);
-    note_launch();
-    if (launch_pdl(kern, dim3(static_cast<unsigned>(units)), dim3(kLpThreads), smem, stream, 1, a) != cudaSuccess)
-      st = GH_ERR_CUDA;
-    if (st == GH_OK && a.slices > 1) {
-      const unsigned grid = static_cast<unsigned>(tmin<int64_t>((o.B + kMergeWarps - 1) / kMergeWarps, 8 * sms));
-      note_launch();
-      const StatKernel merge = es == 4 ? static_cast<StatKernel>(logprobs_merge_kernel<float>)
-                                       : static_cast<StatKernel>(logprobs_merge_kernel<uint16_t>);
-      if (launch_pdl(merge, dim3(grid), dim3(32 * kMergeWarps), 0, stream, 1, a) != cudaSuccess) st = GH_ERR_CUDA;
-    }
-  }
-  scratch_free(scratch, stream);
-  return st;
+  const LogprobKernel kern = es == 4 ? logprobs_kernel_for<float>(top, S > 1) : logprobs_kernel_for<uint16_t>(top, S > 1);
+  if (smem > 32 * 1024 && ensure_smem_limit(kern, kLpMaxSegs * 4) != cudaSuccess) return GH_ERR_CUDA;
+  ProfileScope prof(GH_KERNEL_LOGPROBS, stream);
+  note_launch();
+  return launch_pdl(kern, dim3(static_cast<unsigned>(a.B * S)), dim3(kLpThreads), smem, stream, S, a) == cudaSuccess
+             ? GH_OK
+             : GH_ERR_CUDA;
 }
 
 gh_status_t logprobs_vjp_launch(const LogprobVjpArgs& a, gh_dtype_t dtype, cudaStream_t stream) {

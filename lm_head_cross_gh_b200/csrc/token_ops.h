@@ -22,22 +22,11 @@ struct LogprobArgs {
   float* lse;            // [B], of the scaled logits
   float* top_logprob;    // [B, top_k]
   int64_t* top_index;    // [B, top_k]
-};
-
-// Row sums over units (a row, or one of `slices` slices of it): straight to the
-// log-probability outputs (part null), or as partial states to merge.
-struct StatArgs {
-  const void* logits;
-  int64_t B, V, ld;
-  float c;             // log2(e) / temperature
-  uint32_t low;        // lowest logit whose x c is finite (packed bf16, or fp32 bits)
-  int slices;          // per row
-  int slice_segs;      // 512-byte segments per slice
-  int top_k;
-  const int8_t* flags; // [B] 1: the row counts (null: by lp.index)
-  float4* part;        // [B * slices] (reference, sum, weighted sum, -)
-  uint64_t* part_keys; // [B * slices, top_k], 0: none
-  LogprobArgs lp;
+  // set by logprobs_launch
+  uint32_t low;          // lowest logit whose x c is finite (packed bf16, or fp32 bits)
+  int slices;            // CTAs per row
+  int64_t slice_chunks;  // 16-byte chunks per CTA of a row
+  int seg_kind;          // what a segment is
 };
 
 struct LogprobVjpArgs {
