@@ -108,85 +108,154 @@ __device__ __forceinline__ void write_values(const LogprobArgs& o, int64_t row, 
   o.lse[row] = d.none ? kNaN : dist_lse(d, o.temperature);
 }
 
-// The k-th largest of keys[] (n4 groups of four; zeros as padding), found bit by
-// bit, by one warp; stops at a prefix that exactly k keys reach (*exact).  bf16
-// keys differ in their upper 16 bits only.  R > 0: up to 32 R groups, kept in
-// registers.
-template <typename T, int R>
-__device__ __forceinline__ uint32_t kth_key(const uint32_t* keys, int n4, int k, bool* exact) {
-  const int lane = static_cast<int>(threadIdx.x) & 31;
-  const uint4* k4 = reinterpret_cast<const uint4*>(keys);
-  uint4 v[R > 0 ? R : 1];
-  if constexpr (R > 0) {
+// A warp's keys in registers, R groups of four a lane (zeros where there is none).
+template <int R>
+struct LaneKeys {
+  uint4 v[R];
+  __device__ __forceinline__ void load(const uint32_t* keys, int n4) {
+    const int lane = static_cast<int>(threadIdx.x) & 31;
+    const uint4* k4 = reinterpret_cast<const uint4*>(keys);
 #pragma unroll
     for (int i = 0; i < R; ++i) v[i] = 32 * i + lane < n4 ? k4[32 * i + lane] : make_uint4(0, 0, 0, 0);
   }
-  auto reach = [](const uint4& q, uint32_t c) { return (q.x >= c) + (q.y >= c) + (q.z >= c) + (q.w >= c); };
-  constexpr int kLastBit = Elem<T>::kBytes == 2 ? 16 : 0;
-  uint32_t key = 0;
-  *exact = false;
-  for (int bit = 31; bit >= kLastBit; --bit) {
-    const uint32_t cand = key | (1u << bit);
+  // how many of the warp's keys are >= c
+  __device__ __forceinline__ int count(uint32_t c) const {
     int n = 0;
-    if constexpr (R > 0) {
 #pragma unroll
-      for (int i = 0; i < R; ++i) n += reach(v[i], cand);
-    } else {
-      for (int i = lane; i < n4; i += 32) n += reach(k4[i], cand);
-    }
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (n >= k) key = cand;
-    if (n == k) {
-      *exact = true;
-      break;
-    }
+    for (int i = 0; i < R; ++i) n += (v[i].x >= c) + (v[i].y >= c) + (v[i].z >= c) + (v[i].w >= c);
+    return __reduce_add_sync(0xffffffffu, n);
   }
-  return key;
+  __device__ __forceinline__ uint32_t lane_max() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) m = max(m, max(max(v[i].x, v[i].y), max(v[i].z, v[i].w)));
+    return m;
+  }
+  // positions of the keys >= c, in no order; returns how many
+  __device__ __forceinline__ int list_from(uint32_t c, int* list) const {
+    const int lane = static_cast<int>(threadIdx.x) & 31;
+    const uint32_t below = (1u << lane) - 1;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const uint32_t q[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t got = __ballot_sync(0xffffffffu, q[j] >= c);
+        if (q[j] >= c) list[n + __popc(got & below)] = 4 * (32 * i + lane) + j;
+        n += __popc(got);
+      }
+    }
+    return n;
+  }
+};
+
+// The same over keys left in shared memory.
+template <>
+struct LaneKeys<0> {
+  const uint4* k4;
+  int n4;
+  __device__ __forceinline__ void load(const uint32_t* keys, int n) {
+    k4 = reinterpret_cast<const uint4*>(keys);
+    n4 = n;
+  }
+  __device__ __forceinline__ int count(uint32_t c) const {
+    int n = 0;
+    for (int i = static_cast<int>(threadIdx.x) & 31; i < n4; i += 32)
+      n += (k4[i].x >= c) + (k4[i].y >= c) + (k4[i].z >= c) + (k4[i].w >= c);
+    return __reduce_add_sync(0xffffffffu, n);
+  }
+  __device__ __forceinline__ uint32_t lane_max() const {
+    uint32_t m = 0;
+    for (int i = static_cast<int>(threadIdx.x) & 31; i < n4; i += 32) m = max(m, max(max(k4[i].x, k4[i].y), max(k4[i].z, k4[i].w)));
+    return m;
+  }
+  __device__ __forceinline__ int list_from(uint32_t c, int* list) const {
+    const int lane = static_cast<int>(threadIdx.x) & 31;
+    const uint32_t* keys = reinterpret_cast<const uint32_t*>(k4);
+    int n = 0;
+    for (int i = lane; i - lane < 4 * n4; i += 32) {
+      const bool take = i < 4 * n4 && keys[i] >= c;
+      const uint32_t got = __ballot_sync(0xffffffffu, take);
+      if (take) list[n + __popc(got & ((1u << lane) - 1))] = i;
+      n += __popc(got);
+    }
+    return n;
+  }
+};
+
+// The k-th largest of more than k keys, by one warp, in units of 2^kShift (bf16
+// keys differ in their upper 16 bits only): bisection between the least of the
+// lanes' largest keys (32 keys reach it; stepping down from there for larger k)
+// and the largest.  It stops at a value that exactly k keys reach (*exact).
+template <typename T, int R>
+__device__ __forceinline__ uint32_t kth_key(const LaneKeys<R>& keys, int k, bool* exact) {
+  constexpr int kShift = Elem<T>::kBytes == 2 ? 16 : 0;
+  const uint32_t m = keys.lane_max();
+  uint32_t hi = __reduce_max_sync(0xffffffffu, m) >> kShift, lo = __reduce_min_sync(0xffffffffu, m) >> kShift;
+  *exact = false;
+  if (k > 32) {
+    uint32_t step = hi - lo + 1;
+    int n;
+    while ((n = keys.count(lo << kShift)) < k) {
+      hi = lo - 1;
+      lo = lo > step ? lo - step : 0;
+      step *= 2;
+    }
+    *exact = n == k;
+  }
+  while (lo < hi && !*exact) {
+    const uint32_t mid = lo + (hi - lo + 1) / 2;
+    const int n = keys.count(mid << kShift);
+    if (n >= k) lo = mid;
+    else hi = mid - 1;
+    *exact = n == k;
+  }
+  return lo << kShift;
 }
 
 // The first k segments by (key descending, position ascending) of `segs` keys
 // (padded with zeros to a multiple of 128), by one warp: their positions into
 // list[], in no order unless keys tie; returns how many, and in thr a key that
 // k of all the logits reach (0 where there are no more than k segments).
-template <typename T>
-__device__ __forceinline__ int pick_segments(const uint32_t* keys, int segs, int k, int* list, uint32_t* thr) {
+template <typename T, int R>
+__device__ __forceinline__ int pick_from(const uint32_t* keys, int segs, int k, int* list, uint32_t* thr) {
   const int lane = static_cast<int>(threadIdx.x) & 31;
-  if (segs <= k) {
-    for (int i = lane; i < segs; i += 32) list[i] = i;
-    *thr = 0;
-    return segs;
-  }
+  LaneKeys<R> v;
+  v.load(keys, (segs + 3) / 4);
   bool exact;
-  const int n4 = (segs + 3) / 4;
-  const uint32_t key = n4 <= 64 ? kth_key<T, 2>(keys, n4, k, &exact) : kth_key<T, 0>(keys, n4, k, &exact);
+  const uint32_t key = kth_key<T, R>(v, k, &exact);
   *thr = key;
-  const uint32_t below = (1u << lane) - 1;
-  int n = 0;
-  if (exact) {
-    for (int i = 0; i < segs; i += 32) {
-      const bool take = i + lane < segs && keys[i + lane] >= key;
-      const uint32_t got = __ballot_sync(0xffffffffu, take);
-      if (take) list[n + __popc(got & below)] = i + lane;
-      n += __popc(got);
-    }
-    return n;
-  }
+  if (exact) return v.list_from(key, list);
   // Some keys tie at the k-th: all above it, and the first of the equal ones.
   // (A negative bf16 value's key ends in ones: compare the kept bits.)
   const uint32_t mask = Elem<T>::kBytes == 2 ? 0xffff0000u : 0xffffffffu;
-  int above = 0;
+  const uint32_t below = (1u << lane) - 1;
+  int above = 0, n = 0;
   for (int i = lane; i < segs; i += 32) above += (keys[i] & mask) > key;
   int left = k - __reduce_add_sync(0xffffffffu, above);
   for (int i = 0; i < segs && n < k; i += 32) {
-    const uint32_t v = i + lane < segs ? keys[i + lane] & mask : 0u;
-    const uint32_t eq = __ballot_sync(0xffffffffu, v == key);
-    const bool take = v > key || (v == key && __popc(eq & below) < left);
+    const uint32_t q = i + lane < segs ? keys[i + lane] & mask : 0u;
+    const uint32_t eq = __ballot_sync(0xffffffffu, q == key);
+    const bool take = q > key || (q == key && __popc(eq & below) < left);
     const uint32_t got = __ballot_sync(0xffffffffu, take);
     if (take) list[n + __popc(got & below)] = i + lane;
     n += __popc(got);
     left -= tmin(left, __popc(eq));
   }
   return n;
+}
+
+template <typename T>
+__device__ __forceinline__ int pick_segments(const uint32_t* keys, int segs, int k, int* list, uint32_t* thr) {
+  if (segs <= k) {
+    for (int i = static_cast<int>(threadIdx.x) & 31; i < segs; i += 32) list[i] = i;
+    *thr = 0;
+    return segs;
+  }
+  return segs <= 256    ? pick_from<T, 2>(keys, segs, k, list, thr)
+         : segs <= 1024 ? pick_from<T, 8>(keys, segs, k, list, thr)
+                        : pick_from<T, 0>(keys, segs, k, list, thr);
 }
 
 // A threshold key as a logit: keys at or above it are logits >= it.
@@ -405,7 +474,7 @@ __global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_
         offer(key_value(static_cast<uint64_t>(seg_keys[at]) << 32), part.j0 + at);
       }
     } else {
-      constexpr int kAhead = 4;
+      constexpr int kAhead = 8;
       const int per = 32 >> part.shift;  // segments of a warp's load
       for (int i0 = warp * per; i0 < listed; i0 += kLpWarps * kAhead * per) {
         uint4 q[kAhead];
