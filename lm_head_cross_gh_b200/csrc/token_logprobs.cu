@@ -325,7 +325,8 @@ __global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_
   constexpr int ES = Elem<T>::kBytes, EPC = 16 / ES;
   __shared__ LpShared sh;
   __shared__ LpTopShared tsh;
-  extern __shared__ __align__(16) uint32_t seg_keys[];
+  extern __shared__ __align__(16) float seg_max[];  // the segments' largest logits; their keys once picked from
+  uint32_t* const seg_keys = reinterpret_cast<uint32_t*>(seg_max);
   const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
   const int tid = static_cast<int>(threadIdx.x);
   pdl_wait();
@@ -375,9 +376,8 @@ __global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_
     float m[kBatch];
     fold_batch<T, true, TOP == kTopWarp>(sums, q, a.c, a.low, m);
     if constexpr (TOP == kTopWarp) {
-      static_assert(kBatch == 4, "one lane stores each segment's key");
-      const float mine = lane == 0 ? m[0] : lane == 1 ? m[1] : lane == 2 ? m[2] : m[3];
-      if (lane < kBatch) seg_keys[c0 / kSegChunks + lane] = order_key(mine);
+      static_assert(kBatch == 4, "a batch's segments are stored together");
+      if (lane == 0) *reinterpret_cast<float4*>(seg_max + c0 / kSegChunks) = make_float4(m[0], m[1], m[2], m[3]);
     }
     if constexpr (TOP == kTopFine) {
 #pragma unroll
@@ -387,16 +387,16 @@ __global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_
           float v[EPC];
           unpack16<T>(q[i], v);
 #pragma unroll
-          for (int j = 0; j < EPC; ++j) seg_keys[c * EPC + j] = order_key(v[j]);
+          for (int j = 0; j < EPC; ++j) seg_max[c * EPC + j] = v[j];
           continue;
         }
         float v = max_of4<T>(q[i]);
         if (a.seg_kind == kSegQuad) {
           v = f32_max_nan(v, __shfl_xor_sync(0xffffffffu, v, 1));
           v = f32_max_nan(v, __shfl_xor_sync(0xffffffffu, v, 2));
-          if ((lane & 3) == 0) seg_keys[c >> 2] = order_key(v);
+          if ((lane & 3) == 0) seg_max[c >> 2] = v;
         } else {
-          seg_keys[c] = order_key(v);
+          seg_max[c] = v;
         }
       }
     }
@@ -431,8 +431,13 @@ __global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_
   const bool elements = TOP == kTopFine && a.seg_kind == kSegElement;
   if (TOP != kTopNone && warp == 0) {
     const int segs = elements ? nc * EPC : (nc + (1 << part.shift) - 1) >> part.shift;
-    // keys to a multiple of 128 (the last batch's are there already)
-    for (int j = segs + lane; j < (segs + 127) / 128 * 128; j += 32) seg_keys[j] = 0;
+    // keys, zeros up to a multiple of 128
+    uint4* const k4 = reinterpret_cast<uint4*>(seg_keys);
+    for (int j = lane; j < (segs + 127) / 128 * 32; j += 32) {
+      const float4 v = reinterpret_cast<const float4*>(seg_max)[j];
+      k4[j] = make_uint4(4 * j < segs ? order_key(v.x) : 0u, 4 * j + 1 < segs ? order_key(v.y) : 0u,
+                         4 * j + 2 < segs ? order_key(v.z) : 0u, 4 * j + 3 < segs ? order_key(v.w) : 0u);
+    }
     __syncwarp();
     uint32_t thr;
     const int n = pick_segments<T>(seg_keys, segs, a.top_k, sh.list, &thr);
@@ -487,8 +492,8 @@ __global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
           if (c[i] >= nc) continue;
+          if (!(max_of4<T>(q[i]) >= least)) continue;
           uint32_t hits = reach_mask<T>(q[i], least);
-          if (hits == 0) continue;
           float v[EPC];
           unpack16<T>(q[i], v);
           const int64_t j0 = part.j0 + static_cast<int64_t>(c[i]) * EPC;
