@@ -51,6 +51,8 @@ constexpr int kMaxSlices = 8;       // CTAs per row: a portable cluster
 constexpr int kLpMaxSegs = 16384;   // 512-byte segments of a CTA whose keys are kept (64 KiB)
 constexpr int kCandidates = 512;    // logits of the picked segments that reach the threshold, before the slow way
 
+constexpr int kHitChunks = 256;     // chunks with such a logit, before the slow way
+
 // Segments: a warp's load, a quarter of four lanes' loads, one lane's, or one
 // logit.  The finest are for rows with few segments per alternative.
 enum SegKind : int { kSegElement = 0, kSegChunk = 1, kSegQuad = 2, kSegWarp = 3 };
@@ -61,13 +63,15 @@ struct LpShared {
   float4 state[kLpWarps];  // the warps' (reference, sum, weighted sum)
   float4 part;             // this CTA's, read by the cluster's first
   RowDist dist;
-  int count, listed;
+  int count, chunks, listed;
   float least;
   int list[GH_MAX_TOP_K];
 };
 struct LpTopShared {
   uint64_t buf[kCandidates];
   uint64_t out[GH_MAX_TOP_K];  // this CTA's alternatives, largest first, zeros behind them
+  uint4 hit[kHitChunks];       // chunks with a candidate, and which they are
+  int hit_chunk[kHitChunks];
 };
 static_assert(kCandidates >= kTopBuf, "the slow way's buffer");
 static_assert(kMaxSlices * GH_MAX_TOP_K <= 1024, "the keys gathered by a cluster's first CTA");
@@ -266,18 +270,6 @@ __device__ __forceinline__ float least_of(uint32_t thr) {
   return key_value(static_cast<uint64_t>(thr) << 32);
 }
 
-// Which elements of a chunk are >= least (bit j: element j).
-template <typename T>
-__device__ __forceinline__ uint32_t reach_mask(const uint4& q, float least) {
-  constexpr int EPC = 16 / Elem<T>::kBytes;
-  float v[EPC];
-  unpack16<T>(q, v);
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < EPC; ++j) m |= (v[j] >= least ? 1u : 0u) << j;
-  return m;
-}
-
 __device__ __forceinline__ uint64_t ld_dsmem_u64(uint32_t addr) {
   uint64_t v;
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
@@ -421,7 +413,7 @@ __global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_
     }
     if (warp == kEnds) st = combine(st, warp_combine(state_of_element(edge, a.c)));
     if (lane == 0) sh.state[warp] = make_float4(st.r, st.s, st.t, 0.0f);
-    if (TOP != kTopNone && tid == 0) sh.count = 0;
+    if (TOP != kTopNone && tid == 0) sh.count = sh.chunks = 0;
   }
   __syncthreads();
 
@@ -491,22 +483,26 @@ __global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-          if (c[i] >= nc) continue;
-          if (!(max_of4<T>(q[i]) >= least)) continue;
-          uint32_t hits = reach_mask<T>(q[i], least);
-          float v[EPC];
-          unpack16<T>(q[i], v);
-          const int64_t j0 = part.j0 + static_cast<int64_t>(c[i]) * EPC;
-          while (hits) {
-            const int j = __ffs(hits) - 1;
-            hits &= hits - 1;
-            float x = v[0];
-#pragma unroll
-            for (int k = 1; k < EPC; ++k) x = j == k ? v[k] : x;
-            offer(x, j0 + j);
+          if (c[i] >= nc || !(max_of4<T>(q[i]) >= least)) continue;
+          const int p = atomicAdd(&sh.chunks, 1);
+          if (p < kHitChunks) {
+            tsh.hit[p] = q[i];
+            tsh.hit_chunk[p] = c[i];
           }
         }
       }
+      __syncthreads();
+      // (few lanes of a warp have such a chunk: one a thread from here)
+      const int chunks_hit = sh.chunks;
+      for (int i = tid; i < tmin(chunks_hit, kHitChunks); i += kLpThreads) {
+        float v[EPC];
+        unpack16<T>(tsh.hit[i], v);
+        const int64_t j0 = part.j0 + static_cast<int64_t>(tsh.hit_chunk[i]) * EPC;
+#pragma unroll
+        for (int j = 0; j < EPC; ++j)
+          if (v[j] >= least) offer(v[j], j0 + j);
+      }
+      if (tid == 0 && chunks_hit > kHitChunks) atomicAdd(&sh.count, kCandidates + 1);  // the slow way
     }
     if (e >= 0 && edge >= least) offer(edge, e);
     __syncthreads();
