@@ -112,43 +112,37 @@ __device__ __forceinline__ void write_values(const LogprobArgs& o, int64_t row, 
   o.lse[row] = d.none ? kNaN : dist_lse(d, o.temperature);
 }
 
-// A warp's keys in registers, R groups of four a lane (zeros where there is none).
+// A warp's keys in registers: lane l has keys l, l + 32, ... (zeros behind the last).
 template <int R>
 struct LaneKeys {
-  uint4 v[R];
-  __device__ __forceinline__ void load(const uint32_t* keys, int n4) {
+  uint32_t v[R];
+  __device__ __forceinline__ void load(const uint32_t* keys, int segs) {
     const int lane = static_cast<int>(threadIdx.x) & 31;
-    const uint4* k4 = reinterpret_cast<const uint4*>(keys);
 #pragma unroll
-    for (int i = 0; i < R; ++i) v[i] = 32 * i + lane < n4 ? k4[32 * i + lane] : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < R; ++i) v[i] = 32 * i + lane < segs ? keys[32 * i + lane] : 0;
   }
   // how many of the warp's keys are >= c
   __device__ __forceinline__ int count(uint32_t c) const {
     int n = 0;
 #pragma unroll
-    for (int i = 0; i < R; ++i) n += (v[i].x >= c) + (v[i].y >= c) + (v[i].z >= c) + (v[i].w >= c);
+    for (int i = 0; i < R; ++i) n += v[i] >= c ? 1 : 0;
     return __reduce_add_sync(0xffffffffu, n);
   }
   __device__ __forceinline__ uint32_t lane_max() const {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < R; ++i) m = max(m, max(max(v[i].x, v[i].y), max(v[i].z, v[i].w)));
+    for (int i = 0; i < R; ++i) m = max(m, v[i]);
     return m;
   }
-  // positions of the keys >= c, in no order; returns how many
+  // positions of the keys >= c; returns how many
   __device__ __forceinline__ int list_from(uint32_t c, int* list) const {
     const int lane = static_cast<int>(threadIdx.x) & 31;
-    const uint32_t below = (1u << lane) - 1;
     int n = 0;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const uint32_t q[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t got = __ballot_sync(0xffffffffu, q[j] >= c);
-        if (q[j] >= c) list[n + __popc(got & below)] = 4 * (32 * i + lane) + j;
-        n += __popc(got);
-      }
+      const uint32_t got = __ballot_sync(0xffffffffu, v[i] >= c);
+      if (v[i] >= c) list[n + __popc(got & ((1u << lane) - 1))] = 32 * i + lane;
+      n += __popc(got);
     }
     return n;
   }
@@ -157,31 +151,32 @@ struct LaneKeys {
 // The same over keys left in shared memory.
 template <>
 struct LaneKeys<0> {
-  const uint4* k4;
-  int n4;
-  __device__ __forceinline__ void load(const uint32_t* keys, int n) {
-    k4 = reinterpret_cast<const uint4*>(keys);
-    n4 = n;
+  const uint32_t* keys;
+  int segs;
+  __device__ __forceinline__ void load(const uint32_t* from, int n) {
+    keys = from;
+    segs = n;
   }
   __device__ __forceinline__ int count(uint32_t c) const {
+    // (four at a time: zeros fill the keys up to a multiple of 128)
+    const uint4* k4 = reinterpret_cast<const uint4*>(keys);
     int n = 0;
-    for (int i = static_cast<int>(threadIdx.x) & 31; i < n4; i += 32)
+    for (int i = static_cast<int>(threadIdx.x) & 31; 4 * i < segs; i += 32)
       n += (k4[i].x >= c) + (k4[i].y >= c) + (k4[i].z >= c) + (k4[i].w >= c);
     return __reduce_add_sync(0xffffffffu, n);
   }
   __device__ __forceinline__ uint32_t lane_max() const {
     uint32_t m = 0;
-    for (int i = static_cast<int>(threadIdx.x) & 31; i < n4; i += 32) m = max(m, max(max(k4[i].x, k4[i].y), max(k4[i].z, k4[i].w)));
+    for (int i = static_cast<int>(threadIdx.x) & 31; i < segs; i += 32) m = max(m, keys[i]);
     return m;
   }
   __device__ __forceinline__ int list_from(uint32_t c, int* list) const {
     const int lane = static_cast<int>(threadIdx.x) & 31;
-    const uint32_t* keys = reinterpret_cast<const uint32_t*>(k4);
     int n = 0;
-    for (int i = lane; i - lane < 4 * n4; i += 32) {
-      const bool take = i < 4 * n4 && keys[i] >= c;
+    for (int i = 0; i < segs; i += 32) {
+      const bool take = i + lane < segs && keys[i + lane] >= c;
       const uint32_t got = __ballot_sync(0xffffffffu, take);
-      if (take) list[n + __popc(got & ((1u << lane) - 1))] = i;
+      if (take) list[n + __popc(got & ((1u << lane) - 1))] = i + lane;
       n += __popc(got);
     }
     return n;
@@ -220,13 +215,13 @@ __device__ __forceinline__ uint32_t kth_key(const LaneKeys<R>& keys, int k, bool
 
 // The first k segments by (key descending, position ascending) of `segs` keys
 // (padded with zeros to a multiple of 128), by one warp: their positions into
-// list[], in no order unless keys tie; returns how many, and in thr a key that
+// list[], in order; returns how many, and in thr a key that
 // k of all the logits reach (0 where there are no more than k segments).
 template <typename T, int R>
 __device__ __forceinline__ int pick_from(const uint32_t* keys, int segs, int k, int* list, uint32_t* thr) {
   const int lane = static_cast<int>(threadIdx.x) & 31;
   LaneKeys<R> v;
-  v.load(keys, (segs + 3) / 4);
+  v.load(keys, segs);
   bool exact;
   const uint32_t key = kth_key<T, R>(v, k, &exact);
   *thr = key;
@@ -257,8 +252,8 @@ __device__ __forceinline__ int pick_segments(const uint32_t* keys, int segs, int
     *thr = 0;
     return segs;
   }
-  return segs <= 256    ? pick_from<T, 2>(keys, segs, k, list, thr)
-         : segs <= 1024 ? pick_from<T, 8>(keys, segs, k, list, thr)
+  return segs <= 256    ? pick_from<T, 8>(keys, segs, k, list, thr)
+         : segs <= 1024 ? pick_from<T, 32>(keys, segs, k, list, thr)
                         : pick_from<T, 0>(keys, segs, k, list, thr);
 }
 
