@@ -593,8 +593,12 @@ __global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_
 // -inf gives 2^y (a + b y) = 0 as well.  The rounding of lse log2(e) moves to
 // the factor 2^-lo of a and b; fp32 logits add the rounding of c.
 //
-// A CTA takes tiles of a row, four 16-byte chunks a thread; the row's scalars
-// and the chunks are loaded together, so a tile waits for memory once.
+// One CTA of four warps per part of a row (parts of about 32 KiB), eight on an
+// SM; the warps stream batches as the forward does.  Bound by HBM: [8192, 50257]
+// bf16 in 254 us and [1024, 128256] fp32 in 158 us, both at the copy rate.  The
+// parts' size matters because the CTAs in flight then read and write one stretch
+// of memory: 16 KiB 258 / 155 us, 64 KiB 259 / 164, 128 KiB 269 / 167, and whole
+// rows as tiles of one persistent grid 303 / 167.
 // ---------------------------------------------------------------------------
 
 // Beyond this |lse| its fp32 rounding (2^-14 here) would show in exp(x / T -
@@ -602,9 +606,9 @@ __global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_
 // their max and sum taken again.
 constexpr float kFarLse = 1024.0f;
 
-constexpr int kVjpTileThreads = 256;
-constexpr int kVjpTileUnroll = 4;
-constexpr int kVjpTileChunks = kVjpTileThreads * kVjpTileUnroll;
+constexpr int kLpVjpWarps = 4;
+constexpr int kLpVjpThreads = 32 * kLpVjpWarps;
+constexpr int64_t kVjpPartBytes = 32 * 1024;
 
 constexpr float kLog2eLo = static_cast<float>(1.4426950408889634 - static_cast<double>(kLog2e));
 
@@ -612,25 +616,27 @@ struct VjpScalars {
   float sub, hi, a, b, gt, x0;
 };
 
-template <typename T>
+// FAR: rows with sub != 0.
+template <typename T, bool FAR>
 __device__ __forceinline__ float vjp_element(float x, const VjpScalars& w, float c, float c_lo) {
-  x = fmaxf(x - w.sub, w.x0);
+  x = fmaxf(FAR ? x - w.sub : x, w.x0);
   const float y = fmaf(x, c, Elem<T>::kBytes == 4 ? fmaf(x, c_lo, -w.hi) : -w.hi);
   return ex2(y) * fmaf(w.b, y, w.a);
 }
 
-template <typename T>
-__device__ __forceinline__ void vjp_tile_chunk(const uint4& q, const VjpScalars& w, float c, float c_lo, int tj,
-                                               uint8_t* dst, bool congruent) {
+template <typename T, bool FAR>
+__device__ __forceinline__ void lp_vjp_chunk(uint4 q, const VjpScalars& w, uint32_t low, float c, float c_lo, int tj,
+                                          uint8_t* dst, bool congruent) {
   constexpr int ES = Elem<T>::kBytes, EPC = 16 / ES;
+  if (!FAR) q = clamp_low<T>(q, low);
   float v[EPC], g[EPC];
   unpack16<T>(q, v);
   const float2 c2 = make_float2(c, c), l2 = make_float2(c_lo, c_lo), h2 = make_float2(-w.hi, -w.hi),
-               s2 = make_float2(-w.sub, -w.sub), a2 = make_float2(w.a, w.a), b2 = make_float2(w.b, w.b);
+               a2 = make_float2(w.a, w.a), b2 = make_float2(w.b, w.b);
 #pragma unroll
   for (int j = 0; j < EPC; j += 2) {
-    float2 x = __fadd2_rn(make_float2(v[j], v[j + 1]), s2);
-    x = make_float2(fmaxf(x.x, w.x0), fmaxf(x.y, w.x0));
+    float2 x = make_float2(v[j], v[j + 1]);
+    if (FAR) x = make_float2(fmaxf(x.x - w.sub, w.x0), fmaxf(x.y - w.sub, w.x0));
     const float2 y = __ffma2_rn(x, c2, ES == 4 ? __ffma2_rn(x, l2, h2) : h2);
     const float2 r = __fmul2_rn(make_float2(ex2(y.x), ex2(y.y)), __ffma2_rn(b2, y, a2));
     g[j] = r.x;
@@ -650,85 +656,108 @@ __device__ __forceinline__ void vjp_tile_chunk(const uint4& q, const VjpScalars&
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kVjpTileThreads) logprobs_vjp_kernel(LogprobVjpArgs a, int64_t row_tiles) {
+__global__ void __launch_bounds__(kLpVjpThreads, 8) logprobs_vjp_kernel(LogprobVjpArgs a) {
   constexpr int ES = Elem<T>::kBytes;
-  __shared__ float red[2][kVjpTileThreads / 32];
+  __shared__ float red[2][kLpVjpWarps];
   pdl_wait();
   pdl_trigger();
-  const int tid = static_cast<int>(threadIdx.x);
-  for (int64_t tile = blockIdx.x; tile < a.B * row_tiles; tile += gridDim.x) {
-    const int64_t row = tile / row_tiles, part = tile - row * row_tiles;
-    const RowGeo r = row_geo<ES>(a.logits, row, a.ld, a.V);
-    const int64_t c0 = r.c_lo + part * kVjpTileChunks + tid;
-    uint4 q[kVjpTileUnroll];
+  const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  const int64_t row = a.parts == 1 ? blockIdx.x : blockIdx.x / a.parts;
+  const int part = static_cast<int>(blockIdx.x - row * a.parts);
+  const RowGeo r = row_geo<ES>(a.logits, row, a.ld, a.V);
+  const int64_t from = tmin(r.c_hi, r.c_lo + part * a.part_chunks);
+  int64_t nc = (part == a.parts - 1 ? r.c_hi : tmin(r.c_hi, from + a.part_chunks)) - from;
+  const uint4* const chunks = reinterpret_cast<const uint4*>(r.base) + from + lane;
+  constexpr int kStep = kLpVjpWarps * kBatchChunks;
+  auto load = [&](uint4 (&q)[kBatch], int64_t c0) {
 #pragma unroll
-    for (int u = 0; u < kVjpTileUnroll; ++u) {
-      const int64_t c = c0 + u * kVjpTileThreads;
-      if (c < r.c_hi) q[u] = __ldcs(reinterpret_cast<const uint4*>(r.base + 16 * c));
-    }
-    const int64_t t = a.index[row];
-    uint8_t* dst = static_cast<uint8_t*>(a.grad) + row * a.ld_grad * ES;
-    uint8_t* gbase = dst - r.lead;  // chunk c's gradient bytes start at gbase + 16 c
-    const bool congruent = ((reinterpret_cast<uintptr_t>(dst) ^ reinterpret_cast<uintptr_t>(r.src)) & 15) == 0;
-    // the ragged ends go with the first tile, elements in lanes of its first warp
-    const int64_t e = part == 0 && tid < 32 ? edge_element(r, a.V, tid) : -1;
-    const float edge = e >= 0 ? Elem<T>::load(r.src + e * ES) : 0.0f;
-    VjpScalars w{0.0f, 0.0f, 0.0f, 0.0f, 0.0f, kNegInf};
-    const bool counts = t != a.ignore_index && t >= 0 && t < a.V;
-    bool far = false;
-    if (counts) {
-      const float lse = a.lse[row], gl = a.g_logprob[row], gH = a.g_entropy ? a.g_entropy[row] : 0.0f;
-      const float H = a.entropy[row];
-      w.hi = lse * kLog2e;
-      float lo = fmaf(lse, kLog2e, -w.hi) + lse * kLog2eLo;
-      far = fabsf(lse) > kFarLse;
-      if (far) {
-        if (part != 0) continue;  // the row's first tile takes it whole (in place, its sums come before any store)
-        float m = kNegInf, s = 0.0f;
-        for (int64_t j = tid; j < a.V; j += kVjpTileThreads) m = fmaxf(m, Elem<T>::load(r.src + j * ES));
-        m = block_max<kVjpTileThreads>(m, red[0]);
-        for (int64_t j = tid; j < a.V; j += kVjpTileThreads) s += ex2((Elem<T>::load(r.src + j * ES) - m) * a.c);
-        w.hi = log2f(block_sum<kVjpTileThreads>(s, red[1]));
-        w.sub = m;
-        lo = 0.0f;
-        __syncthreads();
+    for (int i = 0; i < kBatch; ++i)
+      if (c0 + i * kSegChunks + lane < nc) q[i] = __ldcs(chunks + c0 + i * kSegChunks);
+  };
+  uint4 qa[kBatch], qb[kBatch];
+  int64_t c0 = warp * kBatchChunks;
+  load(qa, c0);
+  const int64_t t = a.index[row];
+  const bool counts = t != a.ignore_index && t >= 0 && t < a.V;
+  uint8_t* const dst = static_cast<uint8_t*>(a.grad) + row * a.ld_grad * ES;
+  uint8_t* const gbase = dst - r.lead + 16 * from;  // this part's chunk c's gradient starts at gbase + 16 c
+  const bool congruent = ((reinterpret_cast<uintptr_t>(dst) ^ reinterpret_cast<uintptr_t>(r.src)) & 15) == 0;
+  // the ragged ends go with the first part, elements in lanes of its first warp
+  const int64_t e = part == 0 && warp == 0 ? edge_element(r, a.V, lane) : -1;
+  const float edge = e >= 0 ? Elem<T>::load(r.src + e * ES) : 0.0f;
+  if (!counts) {
+    if (tid == 0 && part == 0 && t != a.ignore_index) record_status(GH_ERR_TARGET_RANGE);
+    for (int64_t c = tid; c < nc; c += kLpVjpThreads) {
+      if (congruent) {
+        __stcs(reinterpret_cast<uint4*>(gbase + 16 * c), make_uint4(0, 0, 0, 0));
+      } else {
+        for (int j = 0; j < 16 / ES; ++j) Elem<T>::store(gbase + 16 * c + j * ES, 0.0f);
       }
-      const float k = ex2(-lo);
-      w.a = -(gl + gH * H) * a.inv_t * k;
-      w.b = -gH * kLn2 * a.inv_t * k;
-      w.gt = gl * a.inv_t;
-      w.x0 = (w.hi - 512.0f) / a.c;
-    } else if (tid == 0 && part == 0 && t != a.ignore_index) {
-      record_status(GH_ERR_TARGET_RANGE);
     }
-    if (counts) {
-      const int64_t tb = r.lead + t * ES;
-      const int64_t tc = tb >> 4;
-      const int tj = static_cast<int>((tb & 15) / ES);
+    if (e >= 0) Elem<T>::store(dst + e * ES, 0.0f);
+    return;
+  }
+  VjpScalars w;
+  const float lse = a.lse[row], gl = a.g_logprob[row], gH = a.g_entropy ? a.g_entropy[row] : 0.0f;
+  const float H = a.entropy[row];
+  w.hi = lse * kLog2e;
+  w.sub = 0.0f;
+  float lo = fmaf(lse, kLog2e, -w.hi) + lse * kLog2eLo;
+  const bool far = fabsf(lse) > kFarLse;
+  if (far) {
+    // the row's first part takes it whole (in place, its sums come before any store)
+    if (part != 0) return;
+    float m = kNegInf, s = 0.0f;
+    for (int64_t j = tid; j < a.V; j += kLpVjpThreads) m = fmaxf(m, Elem<T>::load(r.src + j * ES));
+    m = block_max<kLpVjpThreads>(m, red[0]);
+    for (int64_t j = tid; j < a.V; j += kLpVjpThreads) s += ex2((Elem<T>::load(r.src + j * ES) - m) * a.c);
+    w.hi = log2f(block_sum<kLpVjpThreads>(s, red[1]));
+    w.sub = m;
+    lo = 0.0f;
+    __syncthreads();
+    nc = r.c_hi - from;
+    load(qa, c0);
+  }
+  const float k = ex2(-lo);
+  w.a = -(gl + gH * H) * a.inv_t * k;
+  w.b = -gH * kLn2 * a.inv_t * k;
+  w.gt = gl * a.inv_t;
+  w.x0 = (w.hi - 512.0f) / a.c;
+  // (not far: |hi| < 1478, so x0's rounding to bf16 moves y by less than 8 there)
+  const uint32_t low = ES == 4 ? __float_as_uint(w.x0) : pack_bf16x2(w.x0, w.x0);
+  const int64_t tb = r.lead + t * ES - 16 * from;  // the given token's byte in this part
+  const int64_t tc = tb >> 4;
+  const int tj = static_cast<int>((tb & 15) / ES);
+  auto put = [&](const uint4 (&q)[kBatch], int64_t at) {
+    uint8_t* const p = gbase + 16 * (at + lane);
+    const int64_t ti = tc - at - lane;  // 32 i: the token lies in this lane's chunk i
+    if (!far && at + kBatchChunks <= nc) {
 #pragma unroll
-      for (int u = 0; u < kVjpTileUnroll; ++u) {
-        const int64_t c = c0 + u * kVjpTileThreads;
-        if (c < r.c_hi) vjp_tile_chunk<T>(q[u], w, a.c, a.c_lo, c == tc ? tj : -1, gbase + 16 * c, congruent);
-      }
-      if (far) {
-        for (int64_t c = c0 + kVjpTileChunks; c < r.c_hi; c += kVjpTileThreads)
-          vjp_tile_chunk<T>(__ldcs(reinterpret_cast<const uint4*>(r.base + 16 * c)), w, a.c, a.c_lo, c == tc ? tj : -1,
-                            gbase + 16 * c, congruent);
-      }
-      if (e >= 0) Elem<T>::store(dst + e * ES, vjp_element<T>(edge, w, a.c, a.c_lo) + (e == t ? w.gt : 0.0f));
+      for (int i = 0; i < kBatch; ++i)
+        lp_vjp_chunk<T, false>(q[i], w, low, a.c, a.c_lo, ti == i * kSegChunks ? tj : -1, p + 16 * kSegChunks * i, congruent);
     } else {
-#pragma unroll
-      for (int u = 0; u < kVjpTileUnroll; ++u) {
-        const int64_t c = c0 + u * kVjpTileThreads;
-        if (c >= r.c_hi) break;
-        if (congruent) {
-          __stcs(reinterpret_cast<uint4*>(gbase + 16 * c), make_uint4(0, 0, 0, 0));
-        } else {
-          for (int j = 0; j < 16 / ES; ++j) Elem<T>::store(gbase + 16 * c + j * ES, 0.0f);
-        }
+#pragma unroll 1
+      for (int i = 0; i < kBatch; ++i) {
+        if (at + i * kSegChunks + lane >= nc) break;
+        const uint4 qi = i == 0 ? q[0] : i == 1 ? q[1] : i == 2 ? q[2] : q[3];
+        const int tji = ti == i * kSegChunks ? tj : -1;
+        if (far) lp_vjp_chunk<T, true>(qi, w, low, a.c, a.c_lo, tji, p + 16 * kSegChunks * i, congruent);
+        else lp_vjp_chunk<T, false>(qi, w, low, a.c, a.c_lo, tji, p + 16 * kSegChunks * i, congruent);
       }
-      if (e >= 0) Elem<T>::store(dst + e * ES, 0.0f);
     }
+  };
+  while (c0 < nc) {
+    if (c0 + kStep < nc) load(qb, c0 + kStep);
+    put(qa, c0);
+    c0 += kStep;
+    if (c0 >= nc) break;
+    if (c0 + kStep < nc) load(qa, c0 + kStep);
+    put(qb, c0);
+    c0 += kStep;
+  }
+  if (e >= 0) {
+    const float g = far ? vjp_element<T, true>(edge, w, a.c, a.c_lo) : vjp_element<T, false>(edge, w, a.c, a.c_lo);
+    Elem<T>::store(dst + e * ES, g + (e == t ? w.gt : 0.0f));
   }
 }
 
@@ -801,17 +830,22 @@ gh_status_t logprobs_launch(const LogprobArgs& args, gh_dtype_t dtype, cudaStrea
              : GH_ERR_CUDA;
 }
 
-gh_status_t logprobs_vjp_launch(const LogprobVjpArgs& a, gh_dtype_t dtype, cudaStream_t stream) {
-  const int es = dtype == GH_F32 ? 4 : 2;
-  const int64_t row_tiles = tmax<int64_t>(1, (a.V * es / 16 + kVjpTileChunks - 1) / kVjpTileChunks);
-  const unsigned grid = static_cast<unsigned>(tmin<int64_t>(a.B * row_tiles, static_cast<int64_t>(token_sm_count()) * 8));
+gh_status_t logprobs_vjp_launch(const LogprobVjpArgs& args, gh_dtype_t dtype, cudaStream_t stream) {
+  LogprobVjpArgs a = args;
+  const int64_t bytes = a.V * (dtype == GH_F32 ? 4 : 2);
+  // parts of about kVjpPartBytes; smaller ones, down to 8 KiB, while the CTAs are fewer than are resident
+  const int64_t resident = static_cast<int64_t>(token_sm_count()) * 8;
+  int64_t parts = (bytes + kVjpPartBytes - 1) / kVjpPartBytes;
+  while (a.B * parts < resident && bytes / (2 * parts) >= 8 * 1024) parts *= 2;
+  a.parts = static_cast<int>(parts);
+  a.part_chunks = (bytes / 16 + parts - 1) / parts;
+  if (a.B * parts > INT32_MAX) return GH_ERR_UNSUPPORTED;
   ProfileScope prof(GH_KERNEL_LOGPROBS_VJP, stream);
   note_launch();
-  const cudaError_t e =
-      dtype == GH_F32
-          ? launch_pdl(logprobs_vjp_kernel<float>, dim3(grid), dim3(kVjpTileThreads), 0, stream, 1, a, row_tiles)
-          : launch_pdl(logprobs_vjp_kernel<uint16_t>, dim3(grid), dim3(kVjpTileThreads), 0, stream, 1, a, row_tiles);
-  return e == cudaSuccess ? GH_OK : GH_ERR_CUDA;
+  const auto kern = dtype == GH_F32 ? logprobs_vjp_kernel<float> : logprobs_vjp_kernel<uint16_t>;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(a.B * parts)), dim3(kLpVjpThreads), 0, stream, 1, a) == cudaSuccess
+             ? GH_OK
+             : GH_ERR_CUDA;
 }
 
 }  // namespace gh

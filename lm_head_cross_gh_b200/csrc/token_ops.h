@@ -38,6 +38,9 @@ struct LogprobVjpArgs {
   float c, c_lo;  // log2(e) / temperature as a sum of two floats
   float inv_t;    // 1 / temperature
   const float *lse, *entropy, *g_logprob, *g_entropy;  // [B] (g_entropy may be null)
+  // set by logprobs_vjp_launch
+  int parts;            // CTAs per row
+  int64_t part_chunks;  // 16-byte chunks each
 };
 
 struct DistillArgs {
