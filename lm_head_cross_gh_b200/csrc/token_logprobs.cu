@@ -60,8 +60,8 @@ enum SegKind : int { kSegElement = 0, kSegChunk = 1, kSegQuad = 2, kSegWarp = 3 
 enum TopMode : int { kTopNone = 0, kTopWarp = 1, kTopFine = 2 };
 
 struct LpShared {
-  float4 state[kLpWarps];  // the warps' (reference, sum, weighted sum)
-  float4 part;             // this CTA's, read by the cluster's first
+  LaneSums<kLpWarps, true> sums;
+  float4 part;  // this CTA's (reference, sum, weighted sum), read by the cluster's first
   RowDist dist;
   int count, chunks, listed;
   float least;
@@ -398,18 +398,9 @@ __global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_
     fold(qb, c0);
     c0 += kStep;
   }
-  {
-    const float2 sa = __fadd2_rn(sums.s[0], sums.s[1]), ta = __fadd2_rn(sums.t[0], sums.t[1]);
-    SoftState st{sums.r, sa.x + sa.y, ta.x + ta.y};
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      st.s += __shfl_xor_sync(0xffffffffu, st.s, o);
-      st.t += __shfl_xor_sync(0xffffffffu, st.t, o);
-    }
-    if (warp == kEnds) st = combine(st, warp_combine(state_of_element(edge, a.c)));
-    if (lane == 0) sh.state[warp] = make_float4(st.r, st.s, st.t, 0.0f);
-    if (TOP != kTopNone && tid == 0) sh.count = sh.chunks = 0;
-  }
+  if (warp == kEnds) fold_lanes<true>(sums, edge, a.c);
+  sh.sums.post(warp, lane, sums);
+  if (TOP != kTopNone && tid == 0) sh.count = sh.chunks = 0;
   __syncthreads();
 
   // the last warp merges the sums while warp 0 picks the segments
@@ -434,12 +425,7 @@ __global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_
     }
   }
   if (warp == kEnds) {
-    SoftState all{kNegInf, 0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < kLpWarps; ++i) {
-      const float4 v = sh.state[i];
-      all = combine(all, SoftState{v.x, v.y, v.z});
-    }
+    const SoftState all = sh.sums.merge(lane);
     if (SPLIT) {
       if (lane == 0) sh.part = make_float4(all.r, all.s, all.t, 0.0f);
     } else {

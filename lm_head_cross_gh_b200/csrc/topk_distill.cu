@@ -186,8 +186,8 @@ __device__ __forceinline__ void stored_wait() {
 }
 
 struct DistillShared {
-  float2 state[kDistillWarps];  // the streaming warps' (reference, sum)
-  float2 part;                  // this CTA's, read by the cluster's others
+  LaneSums<kDistillWarps, false> sums;
+  float2 part;  // this CTA's (reference, sum), read by the cluster's others
   RowDist dist;
   float coef;
 };
@@ -230,12 +230,13 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillArgs
   int c0 = first;
   load(qa, c0);  // (before it is known whether the row counts)
   const bool counts = a.flags[row] != 0;
-  int64_t e = -1;  // a ragged-end element, in lanes of the last warp
-  constexpr int kEnds = kDistillWarps;
-  if (warp == kEnds) {
+  constexpr int kEnds = kDistillWarps;  // the warp of the teacher's side
+  int64_t e = -1;  // a ragged-end element, in lanes of the first warp
+  if (warp == 0) {
     e = edge_element(r, a.V, lane);
     if (lane < 16 ? rank != 0 : rank != C - 1) e = -1;
   }
+  float edge = kNegInf;
   if (!counts) {
     if (rank == 0 && tid == 0) a.row_loss[row] = 0.0f;
     if (rank == 0 && warp == kEnds) (void)teacher_row(a, row, lane, true);
@@ -253,9 +254,9 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillArgs
 
   // ---- first pass: the row's sum; the last warp has the teacher's side ----
   Teacher t;
-  float xk[kLaneEntries], edge = kNegInf, scale = 1.0f;
+  float xk[kLaneEntries], scale = 1.0f;
+  if (e >= 0) edge = Elem<T>::load(r.src + e * ES);
   if (warp == kEnds) {
-    if (e >= 0) edge = Elem<T>::load(r.src + e * ES);
     t = teacher_row(a, row, lane, rank == 0);
 #pragma unroll
     for (int i = 0; i < kLaneEntries; ++i) xk[i] = t.id[i] >= 0 ? Elem<T>::load(r.src + static_cast<int64_t>(t.id[i]) * ES) : 0.0f;
@@ -276,19 +277,12 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillArgs
   const bool with_grad = a.grad != nullptr;
   c0 = first;
   if (with_grad) load(qa, c0);
-  if (warp < kDistillWarps) {
-    const float2 sa = __fadd2_rn(sums.s[0], sums.s[1]);
-    const float s = warp_sum(sa.x + sa.y);
-    if (lane == 0) sh.state[warp] = make_float2(sums.r, s);
-  }
+  if (warp == 0) fold_lanes<false>(sums, edge, a.c);
+  if (warp < kDistillWarps) sh.sums.post(warp, lane, sums);
   __syncthreads();
   if (warp == kEnds || C > 1) {
     SoftState st{kNegInf, 0.0f, 0.0f};
-    if (warp == kEnds) {
-      st = state_of_element(edge, a.c);
-      if (lane < kDistillWarps) st = combine(st, SoftState{sh.state[lane].x, sh.state[lane].y, 0.0f});
-      st = warp_combine(st);
-    }
+    if (warp == kEnds) st = sh.sums.merge(lane);
     if (C > 1) {
       if (warp == kEnds && lane == 0) sh.part = make_float2(st.r, st.s);
       __syncwarp();
@@ -355,7 +349,6 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillArgs
       const float p = d.none ? kNaN : ex2(fmaf(xk[i] - d.sub, a.c, -d.r)) / d.s;
       xk[i] = ct * fmaf(t.total, p, -qs[i]);  // the gradient there
     }
-    if (e >= 0) Elem<T>::store(dst + e * ES, coef * ex2(fmaf(edge - d.sub, a.c, -d.r)));
     stored_wait();
     // entries of this CTA's part of the row (in place, their logits were read above)
     const int64_t lo = rank == 0 ? 0 : (16 * from - r.lead) / ES;
@@ -366,6 +359,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillArgs
     return;
   }
   if (!with_grad) return;
+  if (e >= 0) Elem<T>::store(dst + e * ES, coef * ex2(fmaf(edge - d.sub, a.c, -d.r)));
   auto put = [&](const uint4 (&q)[kBatch], int at) {
     uint8_t* const p = gbase + 16 * static_cast<int64_t>(at + lane);
     if (at + kBatchChunks <= nc && d.sub == 0.0f) {
