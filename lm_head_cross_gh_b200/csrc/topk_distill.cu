@@ -10,21 +10,28 @@
 // whose value is -inf is none; a row without entries has no loss and a zero
 // gradient.
 //
-// distill_kernel: 7 streaming warps and one for the teacher's side per row, or
+// distill_kernel: 8 streaming warps and one for the teacher's side per row, or
 // a cluster of such CTAs for long rows and small batches; three CTAs on an SM.
 // The first pass sums 2^(x c - R) as the log-probabilities' forward does; the
 // second reads the row again, from L2 (the rows in flight are a third of it),
 // and stores the dense part scale T Q p_j; then the last warp, which has worked
 // out the teacher's side and the loss meanwhile, stores the K elements that
-// differ.  HBM sees one read and one write of every logit.
+// differ.  HBM sees one read and one write of every logit (271 + 268 MB for a
+// sixth of the bf16 case below).
 //
-// Bound by HBM and the row ends for fp32 ([4096, 50257], 32 entries: 317 us, 5.2
-// TB/s), by the two exponentials of an element for bf16 ([8192, 50257]: 344 us).
-// Warps x CTAs per SM on those two: 7 x 3 as taken, 7 x 4 371 / 327, 9 x 3 356 /
-// 320, 15 x 2 356 / 356, 11 x 2 352 / 342, 5 x 5 393 / 371.  Rows are split over
-// a cluster from 128 KiB on: at 256 KiB the rows in flight outgrow L2 (fp32 382
-// us, [1024, 262144] bf16 270 us against 241), at 64 KiB the exchanges cost more
-// (424 us for the bf16 rows at 7 x 4).
+// [8192, 50257] bf16 with 32 entries: 337 us, [1024, 262144] bf16 with 128: 229
+// us, [4096, 50257] fp32 with 32: 330 us: 4.6 to 5 TB/s of HBM traffic with the
+// special-function unit 59% (fp32 32%) and the issue slots 42% (30%) busy; the
+// second reading of every row through L2 is what a gradient from known sums (254
+// us for the bf16 case) does not have.  Warps x CTAs per SM on the bf16 and fp32
+// cases, before the last changes: 7 x 3 343 / 317, 7 x 4 371 / 327, 9 x 3 356 /
+// 320, 15 x 2 356 / 356, 11 x 2 352 / 342, 5 x 5 393 / 371; 7 to 10 x 3 are now
+// alike.  Rows are split over a cluster from 128 KiB on: at 256 KiB the rows in
+// flight outgrow L2 (fp32 382 us, [1024, 262144] 270 against 241), at 64 KiB the
+// exchanges cost more (424 us for the bf16 rows).  Also tried: sums and
+// gradients as items of 32 KiB handed out in an order that keeps a row in L2
+// (462 / 403 us, the items' ends), a quarter of the exponentials as polynomials
+// (355 us and more).
 #include "ce.h"
 #include "linear_ce.h"
 #include "profile.h"
@@ -35,7 +42,7 @@ namespace gh {
 
 namespace {
 
-constexpr int kDistillWarps = 7;  // that stream the row; one more has the teacher's side
+constexpr int kDistillWarps = 8;  // that stream the row; one more has the teacher's side
 constexpr int kDistillThreads = 32 * (kDistillWarps + 1);
 constexpr int kLaneEntries = GH_MAX_TOP_K / 32;
 constexpr int kCountParts = 64;  // CTAs of the counting kernel
@@ -59,10 +66,12 @@ __global__ void __launch_bounds__(256) distill_count_kernel(const int64_t* __res
   unsigned int n = 0;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + warp; row < B; row += static_cast<int64_t>(gridDim.x) * 8) {
     bool any = false;
-    for (int k0 = 0; k0 < K && !any; k0 += 32) {
+    for (int k0 = 0; k0 < K; k0 += 32) {
       const int k = k0 + lane;
-      const bool has = k < K && distill_entry(ids[row * K + k], values[row * K + k], V);
-      any = __any_sync(0xffffffffu, has);
+      const int64_t id = k < K ? ids[row * K + k] : -1;
+      if (id < -1 || id >= V) record_status(GH_ERR_TARGET_RANGE);
+      const bool has = id >= 0 && distill_entry(id, values[row * K + k], V);
+      any |= __any_sync(0xffffffffu, has);
     }
     n += any ? 1 : 0;
     if (flags && lane == 0) flags[row] = any ? 1 : 0;
@@ -90,11 +99,12 @@ __device__ __forceinline__ float distill_scale(const DistillArgs& a, int lane) {
   return 1.0f / static_cast<float>(n > 0 ? n : 1ull);
 }
 
-// The teacher's side of a row, by one warp: lane l has entries l, l + 32, ...
+// The teacher's side of a row, in shared memory (registers would be held by the
+// streaming warps too).
 struct Teacher {
-  int id[kLaneEntries];  // -1: none
-  float log_q[kLaneEntries], q[kLaneEntries];
-  float total;  // Q
+  int id[GH_MAX_TOP_K];  // -1: none
+  float log_q[GH_MAX_TOP_K], q[GH_MAX_TOP_K];
+  float x[GH_MAX_TOP_K];  // the student's logit at the entry
 };
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -103,24 +113,31 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ Teacher teacher_row(const DistillArgs& a, int64_t row, int lane, bool report) {
-  Teacher t;
+// Fills it, by one warp, lane l with entries l, l + 32, ...; returns Q.
+template <typename T>
+__device__ __forceinline__ float teacher_row(const DistillArgs& a, Teacher& t, int64_t row, const uint8_t* src, int lane) {
+  int id[kLaneEntries];
+  float log_q[kLaneEntries], q[kLaneEntries];
   float vm = kNegInf;
 #pragma unroll
   for (int i = 0; i < kLaneEntries; ++i) {
     const int k = lane + 32 * i;
-    t.id[i] = -1;
-    t.log_q[i] = kNegInf;
+    id[i] = -1;
+    log_q[i] = kNegInf;
     if (k < a.K) {
-      const int64_t id = a.ids[row * a.K + k];
+      const int64_t id64 = a.ids[row * a.K + k];
       const float v = a.values[row * a.K + k];
-      if (report && (id < -1 || id >= a.V)) record_status(GH_ERR_TARGET_RANGE);
-      if (distill_entry(id, v, a.V)) {
-        t.id[i] = static_cast<int>(id);
-        t.log_q[i] = v;
+      if (distill_entry(id64, v, a.V)) {
+        id[i] = static_cast<int>(id64);
+        log_q[i] = v;
         vm = fmaxf(vm, v);
       }
     }
+  }
+#pragma unroll
+  for (int i = 0; i < kLaneEntries; ++i) {
+    t.id[lane + 32 * i] = id[i];
+    if (id[i] >= 0) t.x[lane + 32 * i] = Elem<T>::load(src + static_cast<int64_t>(id[i]) * Elem<T>::kBytes);
   }
   float sum = 0.0f;
   if (a.renormalize) {
@@ -128,27 +145,33 @@ __device__ __forceinline__ Teacher teacher_row(const DistillArgs& a, int64_t row
     for (int o = 16; o > 0; o >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
 #pragma unroll
     for (int i = 0; i < kLaneEntries; ++i) {
-      t.log_q[i] = t.id[i] >= 0 ? (t.log_q[i] - vm) / a.temperature : kNegInf;
-      t.q[i] = t.id[i] >= 0 ? expf(t.log_q[i]) : 0.0f;
-      sum += t.q[i];
+      log_q[i] = id[i] >= 0 ? (log_q[i] - vm) / a.temperature : kNegInf;
+      q[i] = id[i] >= 0 ? expf(log_q[i]) : 0.0f;
+      sum += q[i];
     }
     sum = warp_sum(sum);
     const float log_sum = logf(sum);
 #pragma unroll
     for (int i = 0; i < kLaneEntries; ++i) {
-      t.log_q[i] -= log_sum;
-      t.q[i] /= sum;
+      log_q[i] -= log_sum;
+      q[i] /= sum;
     }
-    t.total = sum == sum ? 1.0f : sum;  // (a NaN value makes the row NaN)
+    if (sum == sum) sum = 1.0f;  // (a NaN value makes the row NaN)
   } else {
 #pragma unroll
     for (int i = 0; i < kLaneEntries; ++i) {
-      t.q[i] = t.id[i] >= 0 ? expf(t.log_q[i]) : 0.0f;
-      sum += t.q[i];
+      q[i] = id[i] >= 0 ? expf(log_q[i]) : 0.0f;
+      sum += q[i];
     }
-    t.total = warp_sum(sum);
+    sum = warp_sum(sum);
   }
-  return t;
+#pragma unroll
+  for (int i = 0; i < kLaneEntries; ++i) {
+    t.log_q[lane + 32 * i] = log_q[i];
+    t.q[lane + 32 * i] = q[i];
+  }
+  __syncwarp();
+  return sum;
 }
 
 // Gradient of a chunk's dense part: coef 2^y, y = (x - sub) c - r.
@@ -187,6 +210,7 @@ __device__ __forceinline__ void stored_wait() {
 
 struct DistillShared {
   LaneSums<kDistillWarps, false> sums;
+  Teacher teacher;
   float2 part;  // this CTA's (reference, sum), read by the cluster's others
   RowDist dist;
   float coef;
@@ -225,6 +249,11 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillArgs
       }
     }
   };
+  auto load_last = [&](uint4 (&q)[kBatch], int c0) {  // the second pass's: the lines may leave L2 then
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (c0 + i * kSegChunks + lane < nc) q[i] = __ldcs(chunks + c0 + i * kSegChunks);
+  };
   uint4 qa[kBatch], qb[kBatch];
   const int first = warp < kDistillWarps ? warp * kBatchChunks : nc;
   int c0 = first;
@@ -239,7 +268,6 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillArgs
   float edge = kNegInf;
   if (!counts) {
     if (rank == 0 && tid == 0) a.row_loss[row] = 0.0f;
-    if (rank == 0 && warp == kEnds) (void)teacher_row(a, row, lane, true);
     if (!a.grad) return;
     for (int c = tid; c < nc; c += kDistillThreads) {
       if (congruent) {
@@ -253,14 +281,12 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillArgs
   }
 
   // ---- first pass: the row's sum; the last warp has the teacher's side ----
-  Teacher t;
-  float xk[kLaneEntries], scale = 1.0f;
+  Teacher& t = sh.teacher;
+  float ct = 1.0f, total = 0.0f;  // scale T, Q
   if (e >= 0) edge = Elem<T>::load(r.src + e * ES);
   if (warp == kEnds) {
-    t = teacher_row(a, row, lane, rank == 0);
-#pragma unroll
-    for (int i = 0; i < kLaneEntries; ++i) xk[i] = t.id[i] >= 0 ? Elem<T>::load(r.src + static_cast<int64_t>(t.id[i]) * ES) : 0.0f;
-    scale = distill_scale(a, lane);
+    total = teacher_row<T>(a, t, row, r.src, lane);
+    ct = distill_scale(a, lane) * a.temperature;
   }
   WarpSums sums{kNegInf, kNegInf, {}, {}};
   float m_unused[kBatch];
@@ -276,7 +302,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillArgs
   // the second pass's first loads cross the exchange below
   const bool with_grad = a.grad != nullptr;
   c0 = first;
-  if (with_grad) load(qa, c0);
+  if (with_grad) load_last(qa, c0);
   if (warp == 0) fold_lanes<false>(sums, edge, a.c);
   if (warp < kDistillWarps) sh.sums.post(warp, lane, sums);
   __syncthreads();
@@ -301,7 +327,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillArgs
       const RowDist d = row_dist<T>(st, r.src, a.V, a.c);
       if (lane == 0) {
         sh.dist = d;
-        sh.coef = d.none ? kNaN : scale * a.temperature * t.total / d.s;
+        sh.coef = d.none ? kNaN : ct * total / d.s;
       }
     }
   }
@@ -320,42 +346,30 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillArgs
   if (warp == kEnds) {
     if (rank == 0) {
       float loss = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kLaneEntries; ++i) {
-        const float lp = d.none ? kNaN : kLn2 * log2_p<T>(d, xk[i], a.c);
-        if (t.id[i] >= 0 && !(t.q[i] == 0.0f)) loss = fmaf(t.q[i], t.log_q[i] - lp, loss);
+      for (int k = lane; k < a.K; k += 32) {
+        const float lp = d.none ? kNaN : kLn2 * log2_p<T>(d, t.x[k], a.c);
+        if (t.id[k] >= 0 && !(t.q[k] == 0.0f)) loss = fmaf(t.q[k], t.log_q[k] - lp, loss);
       }
       loss = warp_sum(loss);
       if (lane == 0) a.row_loss[row] = a.temperature * a.temperature * loss;
     }
     if (!with_grad) return;
-    // Q p less the q of every entry with this id
-    float qs[kLaneEntries];
-#pragma unroll
-    for (int i = 0; i < kLaneEntries; ++i) qs[i] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kLaneEntries; ++i) {
-      if (32 * i >= a.K) break;
-      for (int l = 0; l < tmin(32, a.K - 32 * i); ++l) {
-        const int id = __shfl_sync(0xffffffffu, t.id[i], l);
-        const float q = __shfl_sync(0xffffffffu, t.q[i], l);
-#pragma unroll
-        for (int j = 0; j < kLaneEntries; ++j) qs[j] += t.id[j] == id ? q : 0.0f;
-      }
-    }
-    const float ct = scale * a.temperature;
-#pragma unroll
-    for (int i = 0; i < kLaneEntries; ++i) {
-      const float p = d.none ? kNaN : ex2(fmaf(xk[i] - d.sub, a.c, -d.r)) / d.s;
-      xk[i] = ct * fmaf(t.total, p, -qs[i]);  // the gradient there
-    }
-    stored_wait();
-    // entries of this CTA's part of the row (in place, their logits were read above)
+    // the gradient at the entries of this CTA's part of the row: Q p less the q
+    // of every entry with that id (in place, their logits were read above)
     const int64_t lo = rank == 0 ? 0 : (16 * from - r.lead) / ES;
     const int64_t hi = rank == C - 1 ? a.V : (16 * (from + nc) - r.lead) / ES;
-#pragma unroll
-    for (int i = 0; i < kLaneEntries; ++i)
-      if (t.id[i] >= 0 && t.id[i] >= lo && t.id[i] < hi) Elem<T>::store(dst + static_cast<int64_t>(t.id[i]) * ES, xk[i]);
+    for (int k = lane; k < a.K; k += 32) {
+      const int id = t.id[k];
+      float qs = 0.0f;
+      for (int j = 0; j < a.K; ++j) qs += t.id[j] == id ? t.q[j] : 0.0f;
+      const float p = d.none ? kNaN : ex2(fmaf(t.x[k] - d.sub, a.c, -d.r)) / d.s;
+      t.x[k] = ct * fmaf(total, p, -qs);  // (a lane reads and writes its own)
+    }
+    stored_wait();
+    for (int k = lane; k < a.K; k += 32) {
+      const int64_t id = t.id[k];
+      if (id >= 0 && id >= lo && id < hi) Elem<T>::store(dst + id * ES, t.x[k]);
+    }
     return;
   }
   if (!with_grad) return;
@@ -374,11 +388,11 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillArgs
     }
   };
   while (c0 < nc) {
-    if (c0 + kStep < nc) load(qb, c0 + kStep);
+    if (c0 + kStep < nc) load_last(qb, c0 + kStep);
     put(qa, c0);
     c0 += kStep;
     if (c0 >= nc) break;
-    if (c0 + kStep < nc) load(qa, c0 + kStep);
+    if (c0 + kStep < nc) load_last(qa, c0 + kStep);
     put(qb, c0);
     c0 += kStep;
   }
