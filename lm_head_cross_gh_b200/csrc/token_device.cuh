@@ -48,17 +48,18 @@ __device__ __forceinline__ int64_t edge_element(const RowGeo& r, int64_t V, int 
 }
 
 // ---- softmax state -------------------------------------------------------------
-// With c = log2(e) / T and y_j = x_j c - R:  s = sum 2^y_j,  t = sum 2^y_j y_j.
-// R is a rounded product; y_j is one fused multiply-add, so R's rounding moves
-// all terms alike and leaves log p_j = ln 2 (y_j - log2 s).  That holds while
-// |R| <= kFarRef (R's rounding is then at most 2^-5); a state with a larger R
-// carries s = 0, and a row whose largest R is one is summed again from
-// differences to its maximum (far_row).  R = +inf marks a NaN or +inf logit.
+// With c = log2(e) / T and y_j = x_j c - R:  s = sum 2^y_j,  t = sum 2^y_j y_j,
+// and m the largest x.  R is m c rounded; y_j is one fused multiply-add, so R's
+// rounding moves all terms alike.  That holds while |R| <= kFarRef (R's rounding
+// is then at most 2^-5); a state with a larger R carries s = 0, and a row whose
+// largest R is one is summed again from differences to its maximum (far_row).
+// R = +inf marks a NaN or +inf logit.
 constexpr float kFarRef = 1048576.0f;
 
 struct SoftState {
-  float r, s, t;
+  float m, r, s, t;
 };
+constexpr SoftState kNoState{-__builtin_huge_valf(), -__builtin_huge_valf(), 0.0f, 0.0f};
 
 __device__ __forceinline__ float ref_of(float x, float c) {  // x: not NaN
   if (x == kPosInf || x == kNegInf) return x;
@@ -78,38 +79,29 @@ __device__ __forceinline__ SoftState combine(SoftState a, SoftState b) {
   const float r = fmaxf(a.r, b.r);
   rescale(a, r);
   rescale(b, r);
-  return {r, a.s + b.s, a.t + b.t};
+  return {fmaxf(a.m, b.m), r, a.s + b.s, a.t + b.t};
 }
 
-__device__ __forceinline__ SoftState warp_combine(SoftState a) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const SoftState b{__shfl_xor_sync(0xffffffffu, a.r, o), __shfl_xor_sync(0xffffffffu, a.s, o),
-                      __shfl_xor_sync(0xffffffffu, a.t, o)};
-    // both lanes of a pair add in the same order
-    const bool low = ((threadIdx.x & 31) & o) == 0;
-    a = low ? combine(a, b) : combine(b, a);
-  }
-  return a;
-}
-
-__device__ __forceinline__ SoftState state_of_element(float x, float c) {
-  if (x != x) return {kPosInf, 0.0f, 0.0f};
-  const float r = ref_of(x, c);
-  if (!(fabsf(r) <= kFarRef)) return {r, 0.0f, 0.0f};
-  const float y = fmaf(x, c, -r), e = ex2(y);
-  return {r, e, e * y};
-}
-
-// A row's distribution: log p = ln 2 ((x - sub) c - r - l2s).
+// A row's distribution: log p = (x - m) / T - l, and for gradients
+// p = 2^((x - sub) c - r) / s.
 struct RowDist {
-  float sub, r, s, l2s, ts;  // l2s = log2 s, ts = t / s
-  bool none;                 // no distribution
+  float m, l;       // the largest logit; log sum exp((x - m) / T)
+  float sub, r, s;
+  float entropy;
+  bool none;        // no distribution
 };
 
-template <typename T>
-__device__ __forceinline__ float log2_p(const RowDist& d, float x, float c) {
-  return fmaf(x - d.sub, c, -d.r) - d.l2s;
+__device__ __forceinline__ float log_p(const RowDist& d, float x, float temperature) {
+  return (x - d.m) / temperature - d.l;
+}
+
+// l and the entropy from the sums about `r`.  The largest logit's own term is
+// exactly 1 in sum exp((x - m) / T): it is taken out of s as it was added
+// (`own`) and log1p of the rest keeps the digits of rows that are nearly certain.
+__device__ __forceinline__ void finish_dist(RowDist& d, float s, float t, float y_m) {
+  const float own = ex2(y_m);
+  d.l = log1pf(fmaxf(s - own, 0.0f) * ex2(-y_m));
+  d.entropy = d.l - kLn2 * (t / s - y_m);
 }
 
 // A row whose logits all lie far from 0 (lowest-value masks, tiny
@@ -133,20 +125,19 @@ __device__ __noinline__ RowDist far_row(const uint8_t* src, int64_t V, float c) 
     s += __shfl_xor_sync(0xffffffffu, s, o);
     t += __shfl_xor_sync(0xffffffffu, t, o);
   }
-  return {m, 0.0f, s, log2f(s), t / s, false};
+  RowDist d{m, 0.0f, m, 0.0f, s, 0.0f, false};
+  finish_dist(d, s, t, 0.0f);
+  return d;
 }
 
 // The distribution from a row's merged state (the same in every lane).
 template <typename T>
 __device__ __forceinline__ RowDist row_dist(const SoftState& st, const uint8_t* src, int64_t V, float c) {
-  if (st.r == kPosInf || st.r == kNegInf) return {0.0f, 0.0f, 1.0f, 0.0f, 0.0f, true};
+  if (st.r == kPosInf || st.r == kNegInf) return {0.0f, 0.0f, 0.0f, 0.0f, 1.0f, 0.0f, true};
   if (fabsf(st.r) > kFarRef) return far_row<T>(src, V, c);
-  return {0.0f, st.r, st.s, log2f(st.s), st.t / st.s, false};
-}
-
-// log-sum-exp of x / temperature (beyond fp32's range infinite, as its rounding is).
-__device__ __forceinline__ float dist_lse(const RowDist& d, float temperature) {
-  return d.sub / temperature + kLn2 * (d.r + d.l2s);
+  RowDist d{st.m, 0.0f, 0.0f, st.r, st.s, 0.0f, false};
+  finish_dist(d, st.s, st.t, fmaf(st.m, c, -st.r));
+  return d;
 }
 
 // ---- order keys ------------------------------------------------------------------
@@ -354,7 +345,7 @@ __device__ __forceinline__ void fold_lanes(WarpSums& w, float x, float c) {
 // warps lane by lane, and then the 32 lanes from shared memory, in one order.
 template <int W, bool ENT>
 struct LaneSums {
-  float ref[W];
+  float top[W], ref[W];
   float s[W][32], t[ENT ? W : 1][32];
   __align__(16) float lane_s[32], lane_t[32];
 
@@ -365,22 +356,25 @@ struct LaneSums {
       const float2 ta = __fadd2_rn(w.t[0], w.t[1]);
       t[warp][lane] = ta.x + ta.y;
     }
-    if (lane == 0) ref[warp] = w.r;
+    if (lane == 0) {
+      top[warp] = w.m;
+      ref[warp] = w.r;
+    }
   }
 
   // By one warp, after a barrier; every lane gets the state.
   __device__ __forceinline__ SoftState merge(int lane) {
     SoftState v[W];
-    float r = kNegInf;
+    SoftState a = kNoState;
 #pragma unroll
     for (int i = 0; i < W; ++i) {
-      v[i] = {ref[i], s[i][lane], ENT ? t[i][lane] : 0.0f};
-      r = fmaxf(r, v[i].r);
+      v[i] = {top[i], ref[i], s[i][lane], ENT ? t[i][lane] : 0.0f};
+      a.m = fmaxf(a.m, v[i].m);
+      a.r = fmaxf(a.r, v[i].r);
     }
-    SoftState a{r, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < W; ++i) {
-      rescale(v[i], r);
+      rescale(v[i], a.r);
       a.s += v[i].s;
       a.t += v[i].t;
     }
@@ -398,7 +392,7 @@ struct LaneSums {
       }
     }
     __syncwarp();
-    return {r, (ss.x + ss.y) + (ss.z + ss.w), (tt.x + tt.y) + (tt.z + tt.w)};
+    return {a.m, a.r, (ss.x + ss.y) + (ss.z + ss.w), (tt.x + tt.y) + (tt.z + tt.w)};
   }
 };
 

@@ -3,9 +3,10 @@
 //
 // For a row x of V logits, temperature T and c = log2(e) / T, with a reference
 // R near its largest x c,
-//     y_j = x_j c - R,   s = sum_j 2^y_j,   t = sum_j 2^y_j y_j,
-//     log p_j = ln 2 (y_j - log2 s),   lse = ln 2 (R + log2 s),
-//     entropy = ln 2 (log2 s - t / s)
+//     y_j = x_j c - R,   s = sum_j 2^y_j,   t = sum_j 2^y_j y_j,   y_m = M c - R,
+//     l = log sum_j exp((x_j - M) / T) = log1p((s - 2^y_m) 2^-y_m),
+//     log p_j = (x_j - M) / T - l,   lse = M / T + l,
+//     entropy = l - ln 2 (t / s - y_m)
 // (a term with 2^y = 0 adds nothing to t, so -inf logits are 0 log 0 = 0).
 // The alternatives are the top_k logits by (value descending, index
 // ascending); the temperature does not change their order.
@@ -61,7 +62,7 @@ enum TopMode : int { kTopNone = 0, kTopWarp = 1, kTopFine = 2 };
 
 struct LpShared {
   LaneSums<kLpWarps, true> sums;
-  float4 part;  // this CTA's (reference, sum, weighted sum), read by the cluster's first
+  float4 part;  // this CTA's (maximum, reference, sum, weighted sum), read by the cluster's first
   RowDist dist;
   int count, chunks, listed;
   float least;
@@ -98,18 +99,16 @@ __device__ __forceinline__ void write_no_row(const LogprobArgs& o, int64_t row, 
 }
 
 // One alternative of a row.
-template <typename T>
 __device__ __forceinline__ void write_top(const LogprobArgs& o, int64_t row, const RowDist& d, int k, uint64_t key) {
-  o.top_logprob[row * o.top_k + k] = d.none ? kNaN : kLn2 * log2_p<T>(d, key_value(key), o.c);
+  o.top_logprob[row * o.top_k + k] = d.none ? kNaN : log_p(d, key_value(key), o.temperature);
   o.top_index[row * o.top_k + k] = d.none ? -1 : key_index(key);
 }
 
 // Values of a row that counts (by one thread).
-template <typename T>
 __device__ __forceinline__ void write_values(const LogprobArgs& o, int64_t row, const RowDist& d, float xt) {
-  o.logprob[row] = d.none ? kNaN : kLn2 * log2_p<T>(d, xt, o.c);
-  o.entropy[row] = d.none ? kNaN : kLn2 * (d.l2s - d.ts);
-  o.lse[row] = d.none ? kNaN : dist_lse(d, o.temperature);
+  o.logprob[row] = d.none ? kNaN : log_p(d, xt, o.temperature);
+  o.entropy[row] = d.none ? kNaN : d.entropy;
+  o.lse[row] = d.none ? kNaN : d.m / o.temperature + d.l;
 }
 
 // A warp's keys in registers: lane l has keys l, l + 32, ... (zeros behind the last).
@@ -427,11 +426,11 @@ __global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_
   if (warp == kEnds) {
     const SoftState all = sh.sums.merge(lane);
     if (SPLIT) {
-      if (lane == 0) sh.part = make_float4(all.r, all.s, all.t, 0.0f);
+      if (lane == 0) sh.part = make_float4(all.m, all.r, all.s, all.t);
     } else {
       const RowDist d = row_dist<T>(all, r.src, a.V, a.c);
       if (lane == 0) {
-        write_values<T>(a, row, d, xt);
+        write_values(a, row, d, xt);
         if (TOP != kTopNone) sh.dist = d;
       }
     }
@@ -503,7 +502,7 @@ __global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_
     const RowDist d = sh.dist;
     auto put = [&](int place, uint64_t key) {
       if (SPLIT) tsh.out[place] = key;
-      else write_top<T>(a, row, d, place, key);
+      else write_top(a, row, d, place, key);
     };
     for (int i = tid; i < n; i += kLpThreads) {
       const uint64_t key = tsh.buf[i];
@@ -520,14 +519,14 @@ __global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_
     cluster_wait_acquire();
     if (rank == 0) {
       if (warp == kEnds) {
-        SoftState all{kNegInf, 0.0f, 0.0f};
+        SoftState all = kNoState;
         for (int i = 0; i < a.slices; ++i) {
           const uint32_t p = map_to_rank(&sh.part, i);
-          all = combine(all, SoftState{ld_dsmem_f32(p), ld_dsmem_f32(p + 4), ld_dsmem_f32(p + 8)});
+          all = combine(all, SoftState{ld_dsmem_f32(p), ld_dsmem_f32(p + 4), ld_dsmem_f32(p + 8), ld_dsmem_f32(p + 12)});
         }
         const RowDist d = row_dist<T>(all, r.src, a.V, a.c);
         if (lane == 0) {
-          write_values<T>(a, row, d, xt);
+          write_values(a, row, d, xt);
           sh.dist = d;
         }
       }
@@ -557,7 +556,7 @@ __global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_
           const uint64_t key = gathered[sh.list[i]];
           int above = 0;
           for (int j = 0; j < got; ++j) above += gathered[sh.list[j]] > key ? 1 : 0;
-          write_top<T>(a, row, d, above, key);
+          write_top(a, row, d, above, key);
         }
       }
     }

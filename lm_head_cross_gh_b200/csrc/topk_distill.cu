@@ -211,7 +211,7 @@ __device__ __forceinline__ void stored_wait() {
 struct DistillShared {
   LaneSums<kDistillWarps, false> sums;
   Teacher teacher;
-  float2 part;  // this CTA's (reference, sum), read by the cluster's others
+  float4 part;  // this CTA's (maximum, reference, sum, -), read by the cluster's others
   RowDist dist;
   float coef;
 };
@@ -307,19 +307,19 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillArgs
   if (warp < kDistillWarps) sh.sums.post(warp, lane, sums);
   __syncthreads();
   if (warp == kEnds || C > 1) {
-    SoftState st{kNegInf, 0.0f, 0.0f};
+    SoftState st = kNoState;
     if (warp == kEnds) st = sh.sums.merge(lane);
     if (C > 1) {
-      if (warp == kEnds && lane == 0) sh.part = make_float2(st.r, st.s);
+      if (warp == kEnds && lane == 0) sh.part = make_float4(st.m, st.r, st.s, 0.0f);
       __syncwarp();
       cluster_arrive_release();
       cluster_wait_acquire();
       if (warp == kEnds) {
         // every CTA merges the slices in the same order
-        st = {kNegInf, 0.0f, 0.0f};
+        st = kNoState;
         for (int i = 0; i < C; ++i) {
           const uint32_t p = map_to_rank(&sh.part, i);
-          st = combine(st, SoftState{ld_dsmem_f32(p), ld_dsmem_f32(p + 4), 0.0f});
+          st = combine(st, SoftState{ld_dsmem_f32(p), ld_dsmem_f32(p + 4), ld_dsmem_f32(p + 8), 0.0f});
         }
       }
     }
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillArgs
     if (rank == 0) {
       float loss = 0.0f;
       for (int k = lane; k < a.K; k += 32) {
-        const float lp = d.none ? kNaN : kLn2 * log2_p<T>(d, t.x[k], a.c);
+        const float lp = d.none ? kNaN : log_p(d, t.x[k], a.temperature);
         if (t.id[k] >= 0 && !(t.q[k] == 0.0f)) loss = fmaf(t.q[k], t.log_q[k] - lp, loss);
       }
       loss = warp_sum(loss);
