@@ -159,13 +159,13 @@ def _check(status: int, where: str) -> None:
         raise GhError(status, where)
 
 
-def _stream_handle(stream) -> int:
+def _stream_handle(stream, device: Optional[int] = None) -> int:
     import torch
     if stream is None:
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         if raw is not None:  # the handle alone: building a Stream object takes longer than a small kernel's launch
-            return raw(torch.cuda.current_device())
-        stream = torch.cuda.current_stream()
+            return raw(torch.cuda.current_device() if device is None else device)
+        stream = torch.cuda.current_stream(device)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -532,28 +532,37 @@ def gh_selective_log_softmax(logits, index, *, out=None, stream=None):
     return out
 
 
-def _rows(logits):
+def _rows(logits, torch):
     """(B, V, row stride, dtype code) of [B, V] logits whose rows are dense."""
-    import torch
-    _need(logits.dim() == 2 and logits.is_cuda, "logits: CUDA [B, V]")
-    _need(logits.dtype in (torch.float32, torch.bfloat16), "logits dtype must be float32 or bfloat16")
+    _need(logits.is_cuda and logits.dim() == 2, "logits: CUDA [B, V]")
+    dtype = logits.dtype
+    code = GH_F32 if dtype is torch.float32 else GH_BF16 if dtype is torch.bfloat16 else None
+    _need(code is not None, "logits dtype must be float32 or bfloat16")
     B, V = logits.shape
     ld, col = logits.stride()
     _need(V >= 1 and (col == 1 or V == 1), "logits: the last dimension must be dense")
     if B <= 1:
         ld = V
     _need(ld >= V, "logits: rows must not overlap")
-    return B, V, ld, GH_F32 if logits.dtype == torch.float32 else GH_BF16
+    return B, V, ld, code
 
 
 def _row_tensor(t, name: str, dtype, shape, device) -> None:
-    if not (t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+    if not (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
         raise ValueError(f"{name}: contiguous {dtype} {list(shape)} on {device}")
 
 
-def _grad_like(grad, logits, B, V, ld):
+def _row_output(t, name: str, dtype, shape, device, torch, like=None):
+    """An output tensor: the caller's, checked, or a new one (like `like` if given:
+    torch allocates that faster)."""
+    if t is None:
+        return torch.empty(*shape, dtype=dtype, device=device) if like is None else torch.empty_like(like)
+    _row_tensor(t, name, dtype, shape, device)
+    return t
+
+
+def _grad_like(grad, logits, B, V, ld, torch):
     """The gradient's tensor and row stride (by default laid out as the logits)."""
-    import torch
     if grad is None:
         return torch.empty_strided((B, V), (ld, 1), dtype=logits.dtype, device=logits.device), ld
     if grad is logits:
@@ -566,22 +575,17 @@ def _grad_like(grad, logits, B, V, ld):
     return grad, ldg
 
 
-def _on_device_of(fn):
-    """Run `fn` with its first argument's device current (the library launches on
-    the current device, and the default stream is that device's)."""
-    import functools
-
-    @functools.wraps(fn)
-    def call(first, *args, **kwargs):
-        import torch
-        if first.is_cuda and first.device.index != torch.cuda.current_device():
-            with torch.cuda.device(first.device):
-                return fn(first, *args, **kwargs)
-        return fn(first, *args, **kwargs)
-    return call
+def _launch(name: str, device, torch, args, stream) -> None:
+    """Call library function `name` with `device` current (the library launches
+    on the current device), on `stream` or that device's current stream."""
+    fn = getattr(lib(), name)
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream_handle(stream, device.index)), name)
+        return
+    with torch.cuda.device(device):
+        _check(fn(*args, _stream_handle(stream, device.index)), name)
 
 
-@_on_device_of
 def gh_token_logprobs(logits, index, top_k: int = 0, temperature: float = 1.0, ignore_index: int = -100, *,
                       logprob=None, entropy=None, lse=None, top_logprob=None, top_index=None, stream=None):
     """Log-probability of one given token per row, the row's entropy and its
@@ -595,43 +599,28 @@ def gh_token_logprobs(logits, index, top_k: int = 0, temperature: float = 1.0, i
     give 0, 0, 0, -inf and -1.  Outputs are allocated when not given.
     """
     import torch
-    B, V, ld, dtype = _rows(logits)
+    B, V, ld, dtype = _rows(logits, torch)
     dev = logits.device
     _row_tensor(index, "index", torch.int64, (B,), dev)
     top_k = int(top_k)
     _need(0 <= top_k <= V, "top_k must be between 0 and V")
-    f32 = torch.float32
-    if logprob is None:
-        logprob = torch.empty(B, dtype=f32, device=dev)
-    else:
-        _row_tensor(logprob, "logprob", f32, (B,), dev)
-    if entropy is None:
-        entropy = torch.empty(B, dtype=f32, device=dev)
-    else:
-        _row_tensor(entropy, "entropy", f32, (B,), dev)
-    if lse is None:
-        lse = torch.empty(B, dtype=f32, device=dev)
-    else:
-        _row_tensor(lse, "lse", f32, (B,), dev)
+    f32, row = torch.float32, (B,)
+    logprob = _row_output(logprob, "logprob", f32, row, dev, torch)
+    entropy = _row_output(entropy, "entropy", f32, row, dev, torch, logprob)
+    lse = _row_output(lse, "lse", f32, row, dev, torch, logprob)
     if top_k:
-        if top_logprob is None:
-            top_logprob = torch.empty((B, top_k), dtype=f32, device=dev)
-        else:
-            _row_tensor(top_logprob, "top_logprob", f32, (B, top_k), dev)
-        if top_index is None:
-            top_index = torch.empty((B, top_k), dtype=torch.int64, device=dev)
-        else:
-            _row_tensor(top_index, "top_index", torch.int64, (B, top_k), dev)
+        top_logprob = _row_output(top_logprob, "top_logprob", f32, (B, top_k), dev, torch)
+        top_index = _row_output(top_index, "top_index", torch.int64, (B, top_k), dev, torch)
+        tops = (top_logprob.data_ptr(), top_index.data_ptr())
     else:
         top_logprob = top_index = None
-    st = lib().gh_token_logprobs(_ptr(logits), ld, _ptr(index), B, V, dtype, int(ignore_index), float(temperature),
-                                 top_k, _ptr(logprob), _ptr(entropy), _ptr(lse), _ptr(top_logprob), _ptr(top_index),
-                                 _stream_handle(stream))
-    _check(st, "gh_token_logprobs")
+        tops = (None, None)
+    _launch("gh_token_logprobs", dev, torch,
+            (logits.data_ptr(), ld, index.data_ptr(), B, V, dtype, int(ignore_index), float(temperature), top_k,
+             logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), *tops), stream)
     return logprob, entropy, lse, top_logprob, top_index
 
 
-@_on_device_of
 def gh_token_logprobs_vjp(logits, index, lse, entropy, g_logprob, g_entropy=None, temperature: float = 1.0,
                           ignore_index: int = -100, *, grad=None, stream=None):
     """Logits gradient of ``gh_token_logprobs``' log-probability and entropy (one
@@ -644,7 +633,7 @@ def gh_token_logprobs_vjp(logits, index, lse, entropy, g_logprob, g_entropy=None
     logits' row stride when not given.  Returns ``grad``.
     """
     import torch
-    B, V, ld, dtype = _rows(logits)
+    B, V, ld, dtype = _rows(logits, torch)
     dev = logits.device
     _row_tensor(index, "index", torch.int64, (B,), dev)
     _row_tensor(lse, "lse", torch.float32, (B,), dev)
@@ -652,15 +641,13 @@ def gh_token_logprobs_vjp(logits, index, lse, entropy, g_logprob, g_entropy=None
     _row_tensor(g_logprob, "g_logprob", torch.float32, (B,), dev)
     if g_entropy is not None:
         _row_tensor(g_entropy, "g_entropy", torch.float32, (B,), dev)
-    grad, ldg = _grad_like(grad, logits, B, V, ld)
-    st = lib().gh_token_logprobs_vjp(_ptr(logits), ld, _ptr(index), B, V, dtype, int(ignore_index),
-                                     float(temperature), _ptr(lse), _ptr(entropy), _ptr(g_logprob), _ptr(g_entropy),
-                                     _ptr(grad), ldg, _stream_handle(stream))
-    _check(st, "gh_token_logprobs_vjp")
+    grad, ldg = _grad_like(grad, logits, B, V, ld, torch)
+    _launch("gh_token_logprobs_vjp", dev, torch,
+            (logits.data_ptr(), ld, index.data_ptr(), B, V, dtype, int(ignore_index), float(temperature),
+             lse.data_ptr(), entropy.data_ptr(), g_logprob.data_ptr(), _ptr(g_entropy), grad.data_ptr(), ldg), stream)
     return grad
 
 
-@_on_device_of
 def gh_distill_count(teacher_index, teacher_logits, V: int, *, count=None, stream=None):
     """Number of rows with a teacher entry (CUDA int64 scalar tensor): what
     ``gh_topk_distill`` divides a mean by."""
@@ -673,12 +660,11 @@ def gh_distill_count(teacher_index, teacher_logits, V: int, *, count=None, strea
     if count is None:
         count = torch.empty((), dtype=torch.int64, device=dev)
     _need(count.dtype == torch.int64 and count.numel() == 1 and count.device == dev, "count: CUDA int64 scalar")
-    _check(lib().gh_distill_count(_ptr(teacher_index), _ptr(teacher_logits), B, K, int(V), _ptr(count),
-                                  _stream_handle(stream)), "gh_distill_count")
+    _launch("gh_distill_count", dev, torch,
+            (_ptr(teacher_index), _ptr(teacher_logits), B, K, int(V), _ptr(count)), stream)
     return count
 
 
-@_on_device_of
 def gh_topk_distill(logits, teacher_index, teacher_logits, temperature: float = 1.0, renormalize: bool = True,
                     reduction: str = "mean", *, with_grad: bool = True, n_valid_total=None, grad=None, loss=None,
                     row_loss=None, stream=None):
@@ -696,7 +682,7 @@ def gh_topk_distill(logits, teacher_index, teacher_logits, temperature: float = 
     given.  Returns ``(loss, grad)``; ``grad`` is None for ``with_grad=False``.
     """
     import torch
-    B, V, ld, dtype = _rows(logits)
+    B, V, ld, dtype = _rows(logits, torch)
     dev = logits.device
     _need(teacher_index.dim() == 2, "teacher_index: [B, K]")
     K = teacher_index.shape[1]
@@ -705,7 +691,7 @@ def gh_topk_distill(logits, teacher_index, teacher_logits, temperature: float = 
     _need(reduction in GH_REDUCTION, "reduction must be 'mean' or 'sum'")
     ldg = ld
     if with_grad:
-        grad, ldg = _grad_like(grad, logits, B, V, ld)
+        grad, ldg = _grad_like(grad, logits, B, V, ld, torch)
     else:
         _need(grad is None, "grad needs with_grad")
     if loss is None:
@@ -716,11 +702,10 @@ def gh_topk_distill(logits, teacher_index, teacher_logits, temperature: float = 
     if n_valid_total is not None:
         _need(n_valid_total.dtype == torch.int64 and n_valid_total.numel() == 1 and n_valid_total.device == dev,
               "n_valid_total: CUDA int64 scalar")
-    st = lib().gh_topk_distill(_ptr(logits), ld, _ptr(teacher_index), _ptr(teacher_logits), B, V, K, dtype,
-                               float(temperature), 1 if renormalize else 0, GH_REDUCTION[reduction],
-                               _ptr(n_valid_total), _ptr(loss), _ptr(row_loss), _ptr(grad), ldg,
-                               _stream_handle(stream))
-    _check(st, "gh_topk_distill")
+    _launch("gh_topk_distill", dev, torch,
+            (logits.data_ptr(), ld, teacher_index.data_ptr(), teacher_logits.data_ptr(), B, V, K, dtype,
+             float(temperature), 1 if renormalize else 0, GH_REDUCTION[reduction], _ptr(n_valid_total),
+             loss.data_ptr(), _ptr(row_loss), _ptr(grad), ldg), stream)
     return loss, grad
 
 

@@ -57,9 +57,9 @@ struct DistillArgs {
   const unsigned long long* n_valid;  // rows with an entry, of the whole batch (null: counted here)
   float* row_loss;                    // [B] (null: scratch)
   // set by distill_launch
-  unsigned int* parts;        // counts of rows with an entry, to be added
+  unsigned int* parts;        // counts of rows with an entry, to be added (null: counted by each CTA)
   int nparts;
-  int8_t* flags;              // [B] 1: the row has an entry
+  int8_t* flags;              // [B] 1: the row has an entry (null: looked up)
   int cluster;                // CTAs per row
   int64_t slice_chunks;       // 16-byte chunks per CTA of a row
 };

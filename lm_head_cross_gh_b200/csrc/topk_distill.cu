@@ -84,20 +84,33 @@ __global__ void __launch_bounds__(256) distill_count_kernel(const int64_t* __res
   }
 }
 
-// 1 / max(n, 1) of a mean, n given or the sum of the counting kernel's parts
-// (by one warp; the same in every lane).
+// 1 / max(n, 1) of a mean (by one warp; the same in every lane): n given, the
+// sum of the counting kernel's parts, or for a small batch counted here.
 __device__ __forceinline__ float distill_scale(const DistillArgs& a, int lane) {
   if (!a.mean) return 1.0f;
   unsigned long long n = 0;
   if (a.n_valid) {
     n = *a.n_valid;
-  } else {
+  } else if (a.parts) {
     unsigned int m = 0;
     for (int i = lane; i < a.nparts; i += 32) m += a.parts[i];
+    n = __reduce_add_sync(0xffffffffu, m);
+  } else {
+    unsigned int m = 0;
+    for (int row = lane; row < static_cast<int>(a.B); row += 32) {
+      bool any = false;
+      for (int k = 0; k < a.K && !any; ++k) any = distill_entry(a.ids[row * a.K + k], a.values[row * a.K + k], a.V);
+      m += any ? 1 : 0;
+    }
     n = __reduce_add_sync(0xffffffffu, m);
   }
   return 1.0f / static_cast<float>(n > 0 ? n : 1ull);
 }
+
+// Batches up to this many rows count them in every CTA's last warp (two rows a
+// lane, beside the row's first pass) instead of in a kernel of its own: a launch
+// less, 22.1 -> 18.5 us a call at [64, 1024].
+constexpr int64_t kCountInside = 64;
 
 // The teacher's side of a row, in shared memory (registers would be held by the
 // streaming warps too).
@@ -258,7 +271,18 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillArgs
   const int first = warp < kDistillWarps ? warp * kBatchChunks : nc;
   int c0 = first;
   load(qa, c0);  // (before it is known whether the row counts)
-  const bool counts = a.flags[row] != 0;
+  bool counts;
+  if (a.flags) {
+    counts = a.flags[row] != 0;
+  } else {
+    bool has = false;
+    if (tid < a.K) {
+      const int64_t id = a.ids[row * a.K + tid];
+      has = distill_entry(id, a.values[row * a.K + tid], a.V);
+      if (rank == 0 && (id < -1 || id >= a.V)) record_status(GH_ERR_TARGET_RANGE);
+    }
+    counts = __syncthreads_or(has);
+  }
   constexpr int kEnds = kDistillWarps;  // the warp of the teacher's side
   int64_t e = -1;  // a ragged-end element, in lanes of the first warp
   if (warp == 0) {
@@ -436,21 +460,26 @@ gh_status_t distill_count_launch(const int64_t* ids, const float* values, int64_
 gh_status_t distill_launch(const DistillArgs& args, gh_dtype_t dtype, float* loss, cudaStream_t stream) {
   DistillArgs a = args;
   const int es = dtype == GH_F32 ? 4 : 2;
-  // Scratch: the counts, a flag per row, and the row losses unless the caller takes them.
-  const size_t flag_bytes = (static_cast<size_t>(a.B) + 15) / 16 * 16;
+  // Scratch: the counts and a flag per row (larger batches), and the row losses
+  // unless the caller takes them.
+  const bool inside = a.B <= kCountInside;
+  const size_t flag_bytes = inside ? 0 : (static_cast<size_t>(a.B) + 15) / 16 * 16 + 4 * kCountParts;
+  const size_t loss_bytes = a.row_loss ? 0 : static_cast<size_t>(a.B) * sizeof(float);
+  gh_status_t st = GH_OK;
   void* scratch = nullptr;
-  gh_status_t st = scratch_alloc(
-      &scratch, 4 * kCountParts + flag_bytes + (a.row_loss ? 0 : static_cast<size_t>(a.B) * sizeof(float)), stream);
+  if (flag_bytes + loss_bytes > 0) st = scratch_alloc(&scratch, flag_bytes + loss_bytes, stream);
   if (st != GH_OK) return st;
   char* p = static_cast<char*>(scratch);
-  a.parts = reinterpret_cast<unsigned int*>(p);
-  a.flags = reinterpret_cast<int8_t*>(p + 4 * kCountParts);
-  if (!a.row_loss) a.row_loss = reinterpret_cast<float*>(p + 4 * kCountParts + flag_bytes);
-  a.nparts = static_cast<int>(tmin<int64_t>((a.B + 7) / 8, kCountParts));
-  note_launch();
-  if (launch_pdl(distill_count_kernel, dim3(static_cast<unsigned>(a.nparts)), dim3(256), 0, stream, 1, a.ids, a.values,
-                 a.B, a.K, a.V, a.flags, a.parts, static_cast<unsigned long long*>(nullptr)) != cudaSuccess)
-    st = GH_ERR_CUDA;
+  if (!a.row_loss) a.row_loss = reinterpret_cast<float*>(p + flag_bytes);
+  if (!inside) {
+    a.parts = reinterpret_cast<unsigned int*>(p);
+    a.flags = reinterpret_cast<int8_t*>(p + 4 * kCountParts);
+    a.nparts = static_cast<int>(tmin<int64_t>((a.B + 7) / 8, kCountParts));
+    note_launch();
+    if (launch_pdl(distill_count_kernel, dim3(static_cast<unsigned>(a.nparts)), dim3(256), 0, stream, 1, a.ids, a.values,
+                   a.B, a.K, a.V, a.flags, a.parts, static_cast<unsigned long long*>(nullptr)) != cudaSuccess)
+      st = GH_ERR_CUDA;
+  }
 
   // CTAs per row: enough that the rows in flight stay well inside L2 (a CTA's
   // part at most 128 KiB), and for small batches that the SMs have work, down
