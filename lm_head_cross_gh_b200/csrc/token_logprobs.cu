@@ -47,12 +47,20 @@ namespace {
 // ---------------------------------------------------------------------------
 
 constexpr int kLpWarps = 4;
-constexpr int kLpThreads = 32 * kLpWarps;
+// Rows of up to 16 KiB take CTAs of one warp once there are more of them than
+// CTAs of four are resident: the fixed work of a row's end is then one warp's
+// ([4750, 1204] bf16 with 2 alternatives 23.8 -> 14.5 us, [4000, 8192] with 20
+// 33.3 -> 27.6; 32 KiB rows lose: [2000, 16384] 21.2 -> 27.9).
+constexpr int64_t kShortChunks = 1024;
 constexpr int kMaxSlices = 8;       // CTAs per row: a portable cluster
 constexpr int kLpMaxSegs = 16384;   // 512-byte segments of a CTA whose keys are kept (64 KiB)
-constexpr int kCandidates = 512;    // logits of the picked segments that reach the threshold, before the slow way
 
-constexpr int kHitChunks = 256;     // chunks with such a logit, before the slow way
+// How many logits of the picked segments may reach the threshold, and chunks
+// have one, before the slow way.
+template <int W>
+constexpr int kCandidates = W == 1 ? 256 : 512;
+template <int W>
+constexpr int kHitChunks = W == 1 ? 192 : 256;
 
 // Segments: a warp's load, a quarter of four lanes' loads, one lane's, or one
 // logit.  The finest are for rows with few segments per alternative.
@@ -60,21 +68,23 @@ enum SegKind : int { kSegElement = 0, kSegChunk = 1, kSegQuad = 2, kSegWarp = 3 
 // What a kernel keeps for alternatives: nothing, warp segments' keys, or finer ones'.
 enum TopMode : int { kTopNone = 0, kTopWarp = 1, kTopFine = 2 };
 
+template <int W>
 struct LpShared {
-  LaneSums<kLpWarps, true> sums;
+  LaneSums<W, true> sums;
   float4 part;  // this CTA's (maximum, reference, sum, weighted sum), read by the cluster's first
   RowDist dist;
   int count, chunks, listed;
   float least;
   int list[GH_MAX_TOP_K];
 };
+template <int W>
 struct LpTopShared {
-  uint64_t buf[kCandidates];
+  uint64_t buf[kCandidates<W>];
   uint64_t out[GH_MAX_TOP_K];  // this CTA's alternatives, largest first, zeros behind them
-  uint4 hit[kHitChunks];       // chunks with a candidate, and which they are
-  int hit_chunk[kHitChunks];
+  uint4 hit[kHitChunks<W>];    // chunks with a candidate, and which they are
+  int hit_chunk[kHitChunks<W>];
 };
-static_assert(kCandidates >= kTopBuf, "the slow way's buffer");
+static_assert(kCandidates<1> >= kTopBuf && kCandidates<kLpWarps> >= kTopBuf, "the slow way's buffer");
 static_assert(kMaxSlices * GH_MAX_TOP_K <= 1024, "the keys gathered by a cluster's first CTA");
 
 // Rows that count: 1; ignored: 0; an index outside [0, V): -1.
@@ -306,11 +316,16 @@ __device__ __noinline__ int pick_slowly(uint64_t* buf, uint64_t* out, RowPart w,
   return top.n;
 }
 
-template <typename T, int TOP, bool SPLIT>
-__global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_kernel(LogprobArgs a) {
+// CTAs of W warps on an SM (W == 1: as many as 80 registers a thread allow).
+template <int TOP, int W>
+constexpr int kLpResident = W == 1 ? (TOP != kTopNone ? 21 : 24) : (TOP != kTopNone ? 7 : 8);
+
+template <typename T, int TOP, bool SPLIT, int W>
+__global__ void __launch_bounds__(32 * W, kLpResident<TOP, W>) logprobs_kernel(LogprobArgs a) {
+  constexpr int kThreads = 32 * W;
   constexpr int ES = Elem<T>::kBytes, EPC = 16 / ES;
-  __shared__ LpShared sh;
-  __shared__ LpTopShared tsh;
+  __shared__ LpShared<W> sh;
+  __shared__ LpTopShared<W> tsh;
   extern __shared__ __align__(16) float seg_max[];  // the segments' largest logits; their keys once picked from
   uint32_t* const seg_keys = reinterpret_cast<uint32_t*>(seg_max);
   const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
@@ -347,7 +362,7 @@ __global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_
     return;
   }
   // the last warp takes the ragged ends, and with them the row's values
-  constexpr int kEnds = kLpWarps - 1;
+  constexpr int kEnds = W - 1;
   int64_t e = -1;
   float edge = kNegInf, xt = 0.0f;
   if (warp == kEnds) {
@@ -387,7 +402,7 @@ __global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_
       }
     }
   };
-  constexpr int kStep = kLpWarps * kBatchChunks;
+  constexpr int kStep = W * kBatchChunks;
   while (c0 < nc) {
     if (c0 + kStep < nc) load(qb, c0 + kStep);
     fold(qa, c0);
@@ -443,29 +458,29 @@ __global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_
     const float least = sh.least;
     auto offer = [&](float x, int64_t j) {
       const int p = atomicAdd(&sh.count, 1);
-      if (p < kCandidates) tsh.buf[p] = rank_key(order_key(x), j);
+      if (p < kCandidates<W>) tsh.buf[p] = rank_key(order_key(x), j);
     };
     if (elements) {
-      for (int i = tid; i < listed; i += kLpThreads) {
+      for (int i = tid; i < listed; i += kThreads) {
         const int at = sh.list[i];
         offer(key_value(static_cast<uint64_t>(seg_keys[at]) << 32), part.j0 + at);
       }
     } else {
       constexpr int kAhead = 8;
       const int per = 32 >> part.shift;  // segments of a warp's load
-      for (int i0 = warp * per; i0 < listed; i0 += kLpWarps * kAhead * per) {
+      for (int i0 = warp * per; i0 < listed; i0 += W * kAhead * per) {
         uint4 q[kAhead];
         int c[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-          c[i] = listed_chunk(part, sh.list, listed, i0 + i * kLpWarps * per);
+          c[i] = listed_chunk(part, sh.list, listed, i0 + i * W * per);
           if (c[i] < nc) q[i] = __ldcg(part.chunks + c[i]);
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
           if (c[i] >= nc || !(max_of4<T>(q[i]) >= least)) continue;
           const int p = atomicAdd(&sh.chunks, 1);
-          if (p < kHitChunks) {
+          if (p < kHitChunks<W>) {
             tsh.hit[p] = q[i];
             tsh.hit_chunk[p] = c[i];
           }
@@ -474,7 +489,7 @@ __global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_
       __syncthreads();
       // (few lanes of a warp have such a chunk: one a thread from here)
       const int chunks_hit = sh.chunks;
-      for (int i = tid; i < tmin(chunks_hit, kHitChunks); i += kLpThreads) {
+      for (int i = tid; i < tmin(chunks_hit, kHitChunks<W>); i += kThreads) {
         float v[EPC];
         unpack16<T>(tsh.hit[i], v);
         const int64_t j0 = part.j0 + static_cast<int64_t>(tsh.hit_chunk[i]) * EPC;
@@ -482,12 +497,12 @@ __global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_
         for (int j = 0; j < EPC; ++j)
           if (v[j] >= least) offer(v[j], j0 + j);
       }
-      if (tid == 0 && chunks_hit > kHitChunks) atomicAdd(&sh.count, kCandidates + 1);  // the slow way
+      if (tid == 0 && chunks_hit > kHitChunks<W>) atomicAdd(&sh.count, kCandidates<W> + 1);  // the slow way
     }
     if (e >= 0 && edge >= least) offer(edge, e);
     __syncthreads();
     n = sh.count;
-    if (n > kCandidates) {  // the same n in every thread
+    if (n > kCandidates<W>) {  // the same n in every thread
       __syncthreads();
       if (warp == kEnds) {
         n = pick_slowly<T>(tsh.buf, tsh.out, part, sh.list, listed, a.top_k, edge, e);
@@ -504,13 +519,13 @@ __global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_
       if (SPLIT) tsh.out[place] = key;
       else write_top(a, row, d, place, key);
     };
-    for (int i = tid; i < n; i += kLpThreads) {
+    for (int i = tid; i < n; i += kThreads) {
       const uint64_t key = tsh.buf[i];
       int above = 0;
       for (int j = 0; j < n; ++j) above += tsh.buf[j] > key ? 1 : 0;
       if (above < a.top_k) put(above, key);
     }
-    for (int i = tmin(n, a.top_k) + tid; i < a.top_k; i += kLpThreads) put(i, 0);
+    for (int i = tmin(n, a.top_k) + tid; i < a.top_k; i += kThreads) put(i, 0);
   }
   if constexpr (SPLIT) {
     // the cluster's first CTA merges the parts
@@ -535,7 +550,7 @@ __global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_
         // whose segments are single logits
         const int total = a.slices * a.top_k;
         uint64_t* const gathered = reinterpret_cast<uint64_t*>(seg_keys + (total + 127) / 128 * 128);
-        for (int i = tid; i < (total + 127) / 128 * 128; i += kLpThreads) {
+        for (int i = tid; i < (total + 127) / 128 * 128; i += kThreads) {
           uint64_t key = 0;
           if (i < total) {
             key = ld_dsmem_u64(map_to_rank(&tsh.out[i % a.top_k], i / a.top_k));
@@ -552,7 +567,7 @@ __global__ void __launch_bounds__(kLpThreads, TOP != kTopNone ? 7 : 8) logprobs_
         __syncthreads();
         const RowDist d = sh.dist;
         const int got = sh.listed;
-        for (int i = tid; i < got; i += kLpThreads) {
+        for (int i = tid; i < got; i += kThreads) {
           const uint64_t key = gathered[sh.list[i]];
           int above = 0;
           for (int j = 0; j < got; ++j) above += gathered[sh.list[j]] > key ? 1 : 0;
@@ -763,11 +778,16 @@ uint32_t low_bits(float c, int es) {
 
 using LogprobKernel = void (*)(LogprobArgs);
 
+template <typename T, int TOP>
+LogprobKernel logprobs_kernel_for(bool split, bool short_rows) {
+  if (split) return logprobs_kernel<T, TOP, true, kLpWarps>;
+  return short_rows ? logprobs_kernel<T, TOP, false, 1> : logprobs_kernel<T, TOP, false, kLpWarps>;
+}
 template <typename T>
-LogprobKernel logprobs_kernel_for(int top, bool split) {
-  if (top == kTopNone) return split ? logprobs_kernel<T, kTopNone, true> : logprobs_kernel<T, kTopNone, false>;
-  if (top == kTopWarp) return split ? logprobs_kernel<T, kTopWarp, true> : logprobs_kernel<T, kTopWarp, false>;
-  return split ? logprobs_kernel<T, kTopFine, true> : logprobs_kernel<T, kTopFine, false>;
+LogprobKernel logprobs_kernel_for(int top, bool split, bool short_rows) {
+  return top == kTopNone   ? logprobs_kernel_for<T, kTopNone>(split, short_rows)
+         : top == kTopWarp ? logprobs_kernel_for<T, kTopWarp>(split, short_rows)
+                           : logprobs_kernel_for<T, kTopFine>(split, short_rows);
 }
 
 }  // namespace
@@ -780,7 +800,7 @@ gh_status_t logprobs_launch(const LogprobArgs& args, gh_dtype_t dtype, cudaStrea
   a.low = low_bits(a.c, es);
   // CTAs per row: as many as are resident together, each with at least one
   // batch a warp; for alternatives, at most kLpMaxSegs segments each.
-  constexpr int kResident = 7;
+  constexpr int kResident = kLpResident<kTopWarp, kLpWarps>;
   int S = 1;
   while (S < kMaxSlices &&
          ((a.B * S * 2 <= static_cast<int64_t>(sms) * kResident && chunks >= int64_t(2) * S * kLpWarps * kBatchChunks) ||
@@ -806,11 +826,13 @@ gh_status_t logprobs_launch(const LogprobArgs& args, gh_dtype_t dtype, cudaStrea
     smem = static_cast<int>((keys + 127) / 128 * 128 * 4);
     if (S > 1) smem = tmax(smem, (S * k + 127) / 128 * 128 * 4 + S * k * 8);  // keys, and keys with positions
   }
-  const LogprobKernel kern = es == 4 ? logprobs_kernel_for<float>(top, S > 1) : logprobs_kernel_for<uint16_t>(top, S > 1);
+  const bool short_rows = S == 1 && chunks <= kShortChunks && a.B > static_cast<int64_t>(sms) * kResident;
+  const LogprobKernel kern = es == 4 ? logprobs_kernel_for<float>(top, S > 1, short_rows)
+                                     : logprobs_kernel_for<uint16_t>(top, S > 1, short_rows);
   if (smem > 32 * 1024 && ensure_smem_limit(kern, kLpMaxSegs * 4) != cudaSuccess) return GH_ERR_CUDA;
   ProfileScope prof(GH_KERNEL_LOGPROBS, stream);
   note_launch();
-  return launch_pdl(kern, dim3(static_cast<unsigned>(a.B * S)), dim3(kLpThreads), smem, stream, S, a) == cudaSuccess
+  return launch_pdl(kern, dim3(static_cast<unsigned>(a.B * S)), dim3(32 * (short_rows ? 1 : kLpWarps)), smem, stream, S, a) == cudaSuccess
              ? GH_OK
              : GH_ERR_CUDA;
 }

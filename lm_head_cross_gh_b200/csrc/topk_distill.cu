@@ -42,8 +42,12 @@ namespace gh {
 
 namespace {
 
-constexpr int kDistillWarps = 8;  // that stream the row; one more has the teacher's side
-constexpr int kDistillThreads = 32 * (kDistillWarps + 1);
+// Warps that stream a row (one more has the teacher's side); and for rows of up
+// to 32 KiB, once there are more of them than the larger CTAs are resident
+// ([3383, 5056] bf16 with 54 entries 63 -> 34 us, [4000, 16384] with 16 78 -> 70;
+// 64 KiB rows lose: [4000, 32768] 115 -> 140).
+constexpr int kDistillWarps = 8, kDistillShortWarps = 2;
+constexpr int64_t kDistillShortChunks = 2048;
 constexpr int kLaneEntries = GH_MAX_TOP_K / 32;
 constexpr int kCountParts = 64;  // CTAs of the counting kernel
 
@@ -84,9 +88,14 @@ __global__ void __launch_bounds__(256) distill_count_kernel(const int64_t* __res
   }
 }
 
+// Batches of up to this many rows and entries are counted by every CTA itself
+// instead of by a kernel before it: a launch less, 18 -> 15 us a call at [64, 1024].
+constexpr int kCountInside = 64;
+constexpr int64_t kCountInsideEntries = 2048;
+
 // 1 / max(n, 1) of a mean (by one warp; the same in every lane): n given, the
-// sum of the counting kernel's parts, or for a small batch counted here.
-__device__ __forceinline__ float distill_scale(const DistillArgs& a, int lane) {
+// sum of the counting kernel's parts, or the rows marked in has[].
+__device__ __forceinline__ float distill_scale(const DistillArgs& a, const int* has, int lane) {
   if (!a.mean) return 1.0f;
   unsigned long long n = 0;
   if (a.n_valid) {
@@ -97,26 +106,31 @@ __device__ __forceinline__ float distill_scale(const DistillArgs& a, int lane) {
     n = __reduce_add_sync(0xffffffffu, m);
   } else {
     unsigned int m = 0;
-    for (int row = lane; row < static_cast<int>(a.B); row += 32) {
-      bool any = false;
-      for (int k = 0; k < a.K && !any; ++k) any = distill_entry(a.ids[row * a.K + k], a.values[row * a.K + k], a.V);
-      m += any ? 1 : 0;
-    }
+    for (int i = lane; i < static_cast<int>(a.B); i += 32) m += has[i];
     n = __reduce_add_sync(0xffffffffu, m);
   }
   return 1.0f / static_cast<float>(n > 0 ? n : 1ull);
 }
 
-// Batches up to this many rows count them in every CTA's last warp (two rows a
-// lane, beside the row's first pass) instead of in a kernel of its own: a launch
-// less, 22.1 -> 18.5 us a call at [64, 1024].
-constexpr int64_t kCountInside = 64;
+// Marks the rows of a small batch that have an entry (by a whole CTA).
+__device__ __forceinline__ void mark_rows(const DistillArgs& a, int* has, int threads) {
+  const int tid = static_cast<int>(threadIdx.x), B = static_cast<int>(a.B);
+  for (int i = tid; i < B; i += threads) has[i] = 0;
+  __syncthreads();
+  for (int i = tid; i < B * a.K; i += threads) {
+    const int64_t id = a.ids[i];
+    if (distill_entry(id, a.values[i], a.V)) has[i / a.K] = 1;
+    if (blockIdx.x == 0 && (id < -1 || id >= a.V)) record_status(GH_ERR_TARGET_RANGE);
+  }
+  __syncthreads();
+}
 
 // The teacher's side of a row, in shared memory (registers would be held by the
 // streaming warps too).
 struct Teacher {
-  int id[GH_MAX_TOP_K];  // -1: none
-  float log_q[GH_MAX_TOP_K], q[GH_MAX_TOP_K];
+  __align__(16) int id[GH_MAX_TOP_K];  // -1: none
+  __align__(16) float q[GH_MAX_TOP_K];
+  float log_q[GH_MAX_TOP_K];
   float x[GH_MAX_TOP_K];  // the student's logit at the entry
 };
 
@@ -214,25 +228,30 @@ __device__ __forceinline__ void dense_chunk(const uint4& q, float sub, float c, 
 
 // The streaming warps' gradient stores are done (they arrive, the last warp waits).
 constexpr int kStoredBarrier = 1;
+template <int kThreads>
 __device__ __forceinline__ void stored_arrive() {
-  asm volatile("barrier.cta.arrive %0, %1;" ::"n"(kStoredBarrier), "n"(kDistillThreads) : "memory");
+  asm volatile("barrier.cta.arrive %0, %1;" ::"n"(kStoredBarrier), "n"(kThreads) : "memory");
 }
+template <int kThreads>
 __device__ __forceinline__ void stored_wait() {
-  asm volatile("barrier.cta.sync %0, %1;" ::"n"(kStoredBarrier), "n"(kDistillThreads) : "memory");
+  asm volatile("barrier.cta.sync %0, %1;" ::"n"(kStoredBarrier), "n"(kThreads) : "memory");
 }
 
+template <int W>
 struct DistillShared {
-  LaneSums<kDistillWarps, false> sums;
+  LaneSums<W, false> sums;
   Teacher teacher;
   float4 part;  // this CTA's (maximum, reference, sum, -), read by the cluster's others
   RowDist dist;
   float coef;
+  int has[kCountInside];
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillArgs a) {
+template <typename T, int W>
+__global__ void __launch_bounds__(32 * (W + 1), 27 / (W + 1)) distill_kernel(DistillArgs a) {
+  constexpr int kThreads = 32 * (W + 1);
   constexpr int ES = Elem<T>::kBytes;
-  __shared__ DistillShared sh;
+  __shared__ DistillShared<W> sh;
   const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
   const int tid = static_cast<int>(threadIdx.x);
   pdl_wait();
@@ -248,7 +267,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillArgs
   uint8_t* const dst = static_cast<uint8_t*>(a.grad) + row * a.ld_grad * ES;
   uint8_t* const gbase = dst - r.lead + 16 * from;  // this CTA's chunk i's gradient starts at gbase + 16 i
   const bool congruent = ((reinterpret_cast<uintptr_t>(dst) ^ reinterpret_cast<uintptr_t>(r.src)) & 15) == 0;
-  constexpr int kStep = kDistillWarps * kBatchChunks;
+  constexpr int kStep = W * kBatchChunks;
   const uint32_t none = ES == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
   auto load = [&](uint4 (&q)[kBatch], int c0) {
     if (c0 + kBatchChunks <= nc) {
@@ -268,22 +287,12 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillArgs
       if (c0 + i * kSegChunks + lane < nc) q[i] = __ldcs(chunks + c0 + i * kSegChunks);
   };
   uint4 qa[kBatch], qb[kBatch];
-  const int first = warp < kDistillWarps ? warp * kBatchChunks : nc;
+  const int first = warp < W ? warp * kBatchChunks : nc;
   int c0 = first;
   load(qa, c0);  // (before it is known whether the row counts)
-  bool counts;
-  if (a.flags) {
-    counts = a.flags[row] != 0;
-  } else {
-    bool has = false;
-    if (tid < a.K) {
-      const int64_t id = a.ids[row * a.K + tid];
-      has = distill_entry(id, a.values[row * a.K + tid], a.V);
-      if (rank == 0 && (id < -1 || id >= a.V)) record_status(GH_ERR_TARGET_RANGE);
-    }
-    counts = __syncthreads_or(has);
-  }
-  constexpr int kEnds = kDistillWarps;  // the warp of the teacher's side
+  if (!a.flags) mark_rows(a, sh.has, kThreads);
+  const bool counts = (a.flags ? a.flags[row] : sh.has[row]) != 0;
+  constexpr int kEnds = W;  // the warp of the teacher's side
   int64_t e = -1;  // a ragged-end element, in lanes of the first warp
   if (warp == 0) {
     e = edge_element(r, a.V, lane);
@@ -293,7 +302,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillArgs
   if (!counts) {
     if (rank == 0 && tid == 0) a.row_loss[row] = 0.0f;
     if (!a.grad) return;
-    for (int c = tid; c < nc; c += kDistillThreads) {
+    for (int c = tid; c < nc; c += kThreads) {
       if (congruent) {
         __stcs(reinterpret_cast<uint4*>(gbase + 16 * static_cast<int64_t>(c)), make_uint4(0, 0, 0, 0));
       } else {
@@ -310,7 +319,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillArgs
   if (e >= 0) edge = Elem<T>::load(r.src + e * ES);
   if (warp == kEnds) {
     total = teacher_row<T>(a, t, row, r.src, lane);
-    ct = distill_scale(a, lane) * a.temperature;
+    ct = distill_scale(a, sh.has, lane) * a.temperature;
   }
   WarpSums sums{kNegInf, kNegInf, {}, {}};
   float m_unused[kBatch];
@@ -328,7 +337,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillArgs
   c0 = first;
   if (with_grad) load_last(qa, c0);
   if (warp == 0) fold_lanes<false>(sums, edge, a.c);
-  if (warp < kDistillWarps) sh.sums.post(warp, lane, sums);
+  if (warp < W) sh.sums.post(warp, lane, sums);
   __syncthreads();
   if (warp == kEnds || C > 1) {
     SoftState st = kNoState;
@@ -382,18 +391,34 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillArgs
     // of every entry with that id (in place, their logits were read above)
     const int64_t lo = rank == 0 ? 0 : (16 * from - r.lead) / ES;
     const int64_t hi = rank == C - 1 ? a.V : (16 * (from + nc) - r.lead) / ES;
-    for (int k = lane; k < a.K; k += 32) {
-      const int id = t.id[k];
-      float qs = 0.0f;
-      for (int j = 0; j < a.K; ++j) qs += t.id[j] == id ? t.q[j] : 0.0f;
-      const float p = d.none ? kNaN : ex2(fmaf(t.x[k] - d.sub, a.c, -d.r)) / d.s;
-      t.x[k] = ct * fmaf(total, p, -qs);  // (a lane reads and writes its own)
+    int id[kLaneEntries];
+    float qs[kLaneEntries];
+#pragma unroll
+    for (int i = 0; i < kLaneEntries; ++i) {
+      id[i] = t.id[lane + 32 * i];
+      qs[i] = 0.0f;
     }
-    stored_wait();
-    for (int k = lane; k < a.K; k += 32) {
-      const int64_t id = t.id[k];
-      if (id >= 0 && id >= lo && id < hi) Elem<T>::store(dst + id * ES, t.x[k]);
+    for (int j = 0; j < a.K; j += 4) {  // (-1 and 0 behind the K entries)
+      const int4 other = *reinterpret_cast<const int4*>(t.id + j);
+      const float4 q = *reinterpret_cast<const float4*>(t.q + j);
+#pragma unroll
+      for (int i = 0; i < kLaneEntries; ++i) {
+        qs[i] += other.x == id[i] ? q.x : 0.0f;
+        qs[i] += other.y == id[i] ? q.y : 0.0f;
+        qs[i] += other.z == id[i] ? q.z : 0.0f;
+        qs[i] += other.w == id[i] ? q.w : 0.0f;
+      }
     }
+    float fix[kLaneEntries];
+#pragma unroll
+    for (int i = 0; i < kLaneEntries; ++i) {
+      const float p = d.none ? kNaN : ex2(fmaf(t.x[lane + 32 * i] - d.sub, a.c, -d.r)) / d.s;
+      fix[i] = ct * fmaf(total, p, -qs[i]);
+    }
+    stored_wait<kThreads>();
+#pragma unroll
+    for (int i = 0; i < kLaneEntries; ++i)
+      if (id[i] >= 0 && id[i] >= lo && id[i] < hi) Elem<T>::store(dst + static_cast<int64_t>(id[i]) * ES, fix[i]);
     return;
   }
   if (!with_grad) return;
@@ -420,15 +445,17 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillArgs
     put(qb, c0);
     c0 += kStep;
   }
-  stored_arrive();
+  stored_arrive<kThreads>();
 }
 
 // Sum of the row losses in a fixed order, in double, and the mean's division.
 __global__ void __launch_bounds__(1024) distill_reduce_kernel(DistillArgs a, float* loss) {
   __shared__ double red[32];
+  __shared__ int has[kCountInside];
   pdl_wait();
   pdl_trigger();
   const int lane = static_cast<int>(threadIdx.x) & 31;
+  if (a.mean && !a.n_valid && !a.parts) mark_rows(a, has, 1024);
   double s = 0.0;
   for (int64_t i = threadIdx.x; i < a.B; i += 1024) s += static_cast<double>(a.row_loss[i]);
 #pragma unroll
@@ -436,7 +463,7 @@ __global__ void __launch_bounds__(1024) distill_reduce_kernel(DistillArgs a, flo
   if (lane == 0) red[threadIdx.x >> 5] = s;
   __syncthreads();
   if (threadIdx.x < 32) {
-    const double scale = static_cast<double>(distill_scale(a, lane));
+    const double scale = static_cast<double>(distill_scale(a, has, lane));
     s = red[lane];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -462,7 +489,7 @@ gh_status_t distill_launch(const DistillArgs& args, gh_dtype_t dtype, float* los
   const int es = dtype == GH_F32 ? 4 : 2;
   // Scratch: the counts and a flag per row (larger batches), and the row losses
   // unless the caller takes them.
-  const bool inside = a.B <= kCountInside;
+  const bool inside = a.B <= kCountInside && a.B * a.K <= kCountInsideEntries;
   const size_t flag_bytes = inside ? 0 : (static_cast<size_t>(a.B) + 15) / 16 * 16 + 4 * kCountParts;
   const size_t loss_bytes = a.row_loss ? 0 : static_cast<size_t>(a.B) * sizeof(float);
   gh_status_t st = GH_OK;
@@ -496,8 +523,12 @@ gh_status_t distill_launch(const DistillArgs& args, gh_dtype_t dtype, float* los
   if (st == GH_OK) {
     ProfileScope prof(GH_KERNEL_DISTILL, stream);
     note_launch();
-    const auto kern = es == 4 ? distill_kernel<float> : distill_kernel<uint16_t>;
-    if (launch_pdl(kern, dim3(static_cast<unsigned>(a.B * C)), dim3(kDistillThreads), 0, stream, C, a) != cudaSuccess)
+    const bool short_rows = C == 1 && chunks <= kDistillShortChunks && a.B > static_cast<int64_t>(sms) * 3;
+    const int threads = 32 * ((short_rows ? kDistillShortWarps : kDistillWarps) + 1);
+    const auto kern = es == 4 ? (short_rows ? distill_kernel<float, kDistillShortWarps> : distill_kernel<float, kDistillWarps>)
+                              : (short_rows ? distill_kernel<uint16_t, kDistillShortWarps>
+                                            : distill_kernel<uint16_t, kDistillWarps>);
+    if (launch_pdl(kern, dim3(static_cast<unsigned>(a.B * C)), dim3(static_cast<unsigned>(threads)), 0, stream, C, a) != cudaSuccess)
       st = GH_ERR_CUDA;
   }
   if (st == GH_OK) {
