@@ -295,7 +295,8 @@ gh_status_t gh_selective_log_softmax(const void* logits, const int64_t* index, i
  * A row without a distribution (a NaN or +inf logit, or -inf logits only) gets
  * NaN values and alternatives with index -1.  An index outside [0, V) that is
  * not ignore_index: the same, and GH_ERR_TARGET_RANGE is recorded.
- * GH_ERR_UNSUPPORTED for top_k > GH_MAX_TOP_K.
+ * No scratch.  GH_ERR_UNSUPPORTED for top_k > GH_MAX_TOP_K, for top_k > 0 with
+ * rows of more than 64 MiB, and for B of 2^31 and more.
  */
 #define GH_MAX_TOP_K 128
 gh_status_t gh_token_logprobs(const void* logits, int64_t ld, const int64_t* index, int64_t B, int64_t V,
@@ -321,6 +322,7 @@ gh_status_t gh_token_logprobs(const void* logits, int64_t ld, const int64_t* ind
  *            any other overlap is not.
  * Rows whose index equals ignore_index get a zero gradient row; an index
  * outside [0, V) likewise, and records GH_ERR_TARGET_RANGE.  No scratch.
+ * GH_ERR_UNSUPPORTED where B times a row's parts of 32 KiB reaches 2^31.
  */
 gh_status_t gh_token_logprobs_vjp(const void* logits, int64_t ld, const int64_t* index, int64_t B, int64_t V,
                                   gh_dtype_t dtype, int64_t ignore_index, float temperature, const float* lse,
@@ -359,7 +361,9 @@ gh_status_t gh_token_logprobs_vjp(const void* logits, int64_t ld, const int64_t*
  *            grad == logits with ld_grad == ld is allowed; no other overlap.
  * A row without a distribution (see gh_token_logprobs) or with a NaN value
  * gives a NaN loss and gradient row.  An id outside [0, V) other than -1 is
- * treated as none and records GH_ERR_TARGET_RANGE.
+ * treated as none and records GH_ERR_TARGET_RANGE.  Scratch (stream-ordered): at
+ * most 5 bytes a row and 272.  GH_ERR_UNSUPPORTED where B times a
+ * row's CTAs (at most 8) reaches 2^31.
  *
  * gh_distill_count — count = number of rows with an entry (int64 device
  * scalar, written).

@@ -487,6 +487,19 @@ gh_status_t distill_count_launch(const int64_t* ids, const float* values, int64_
 gh_status_t distill_launch(const DistillArgs& args, gh_dtype_t dtype, float* loss, cudaStream_t stream) {
   DistillArgs a = args;
   const int es = dtype == GH_F32 ? 4 : 2;
+  // CTAs per row: enough that the rows in flight stay well inside L2 (a CTA's
+  // part at most 128 KiB), and for small batches that the SMs have work, down
+  // to 8 KiB a CTA.
+  const int64_t chunks = a.V * es / 16;
+  const int sms = token_sm_count();
+  int C = 1;
+  while (C < 8 && (chunks * 16 > C * int64_t(128 * 1024) ||
+                   (a.B * C * 2 <= 2 * sms && chunks * 16 >= 2 * C * int64_t(8 * 1024))))
+    C *= 2;
+  a.cluster = C;
+  a.slice_chunks = (chunks + C - 1) / C;
+  if (a.B * C > INT32_MAX) return GH_ERR_UNSUPPORTED;  // one CTA each
+
   // Scratch: the counts and a flag per row (larger batches), and the row losses
   // unless the caller takes them.
   const bool inside = a.B <= kCountInside && a.B * a.K <= kCountInsideEntries;
@@ -508,18 +521,6 @@ gh_status_t distill_launch(const DistillArgs& args, gh_dtype_t dtype, float* los
       st = GH_ERR_CUDA;
   }
 
-  // CTAs per row: enough that the rows in flight stay well inside L2 (a CTA's
-  // part at most 128 KiB), and for small batches that the SMs have work, down
-  // to 8 KiB a CTA.
-  const int64_t chunks = a.V * es / 16;
-  const int sms = token_sm_count();
-  int C = 1;
-  while (C < 8 && (chunks * 16 > C * int64_t(128 * 1024) ||
-                   (a.B * C * 2 <= 2 * sms && chunks * 16 >= 2 * C * int64_t(8 * 1024))))
-    C *= 2;
-  a.cluster = C;
-  a.slice_chunks = (chunks + C - 1) / C;
-  if (a.B * C > INT32_MAX) st = st == GH_OK ? GH_ERR_UNSUPPORTED : st;
   if (st == GH_OK) {
     ProfileScope prof(GH_KERNEL_DISTILL, stream);
     note_launch();

@@ -304,3 +304,112 @@ def test_selected_value_agrees_with_selective_log_softmax(cuda_device):
     sel = gh.gh_selective_log_softmax(x, t)
     eps = 4e-7 * max(1.0, float(x.abs().max()))
     assert (lp - sel).abs().max().item() <= 4 * eps + 2.0 ** -21 * float(sel.abs().max())
+
+
+def test_keyword_arguments(cuda_device):
+    x, t = logits(5, 333, torch.float32, 61), given(5, 333, 61)
+    out = gh.gh_token_logprobs(logits=x, index=t, top_k=3, temperature=0.9)
+    check_logprobs(x, t, 3, 0.9, out)
+    g = torch.ones(5, device="cuda")
+    a = gh.gh_token_logprobs_vjp(logits=x, index=t, lse=out[2], entropy=out[1], g_logprob=g, temperature=0.9)
+    check_vjp(x, t, g, None, 0.9, a)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B,V,k", [(2, 60001, 20), (20, 33000, 128), (3, 400_003, 7)])
+def test_rows_split_over_a_cluster_with_odd_contents(cuda_device, dtype, B, V, k):
+    """Small batches: a row's CTAs each see a part of it."""
+    x = logits(B, V, dtype, 71, pad=5).round()               # ties across the parts
+    t = given(B, V, 71, 0.0)
+    check_logprobs(x, t, k, 1.0, gh.gh_token_logprobs(x, t, k), what="ties")
+    x[0] = -math.inf
+    x[0, V // 2: V // 2 + 3] = 1.0                            # one part has all the mass
+    check_logprobs(x, t, k, 0.7, gh.gh_token_logprobs(x, t, k, 0.7), what="one part")
+    x[0, 5] = math.nan                                        # and a NaN in another
+    check_logprobs(x, t, k, 0.7, gh.gh_token_logprobs(x, t, k, 0.7), what="NaN")
+    x[0] = math.nan
+    x[1] = torch.finfo(dtype).min
+    check_logprobs(x, t, k, 1.0, gh.gh_token_logprobs(x, t, k), what="all NaN, all lowest")
+    x[0] = torch.arange(V, device="cuda").to(dtype) / 1000    # the last part has every alternative
+    check_logprobs(x, t, k, 1.0, gh.gh_token_logprobs(x, t, k), what="rising")
+
+
+@pytest.mark.parametrize("k", [1, 128])
+def test_more_candidates_than_are_kept(cuda_device, k):
+    """One segment of large equal logits, and a plateau over half the row: more
+    logits reach the threshold than the candidates' buffer holds."""
+    B, V = 1100, 9001
+    x = logits(B, V, torch.bfloat16, 81)
+    x[0, 4000:] = 30.0
+    x[1, 1000:1700] = 30.0
+    x[2, ::3] = 30.0
+    x[3, 3000:3000 + 4 * k] = torch.arange(4 * k, device="cuda").to(torch.bfloat16)
+    t = given(B, V, 81, 0.0)
+    rows = slice(0, 40)
+    out = gh.gh_token_logprobs(x, t, k)
+    check_logprobs(x[rows], t[rows], k, 1.0, [v[rows] for v in out])
+    few = gh.gh_token_logprobs(x[:4], t[:4], k)  # four rows: other kernels
+    check_logprobs(x[:4], t[:4], k, 1.0, few)
+
+
+def test_nearly_certain_rows(cuda_device):
+    """log p near 0 is held to about 1e-7 absolute: the rest's sum, not 1 + rest."""
+    x = logits(64, 50257, torch.float32, 91)
+    t = given(64, 50257, 91, 0.0)
+    x[torch.arange(64), t] = torch.linspace(14.0, 30.0, 64, device="cuda")
+    lp, ent, _, _, _ = gh.gh_token_logprobs(x, t)
+    z = x.double()
+    z[torch.arange(64), t] = -math.inf
+    rest = torch.exp(torch.logsumexp(z, 1) - x.double()[torch.arange(64), t])
+    # 50257 terms in 512 running sums of fp32: the sum that holds the 1 loses at
+    # most 98 half steps of 2^-24, half a step's random walk 10; 2^-20 covers both
+    assert ((lp.double() + torch.log1p(rest)).abs() <= 2.0 ** -20).all()
+    assert (ent >= -2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_vjp_in_place_of_long_and_far_rows(cuda_device, dtype):
+    """Rows of several parts, in place: rows far from 0 have their sums taken again
+    by one of the parts, before any of the row is overwritten."""
+    B, V = 6, 70001
+    x, t = logits(B, V, dtype, 95), given(B, V, 95, 0.0)
+    x[1] -= 30000.0
+    x[2] = torch.finfo(dtype).min
+    for T in (1.0, 0.5):
+        _, ent, lse, _, _ = gh.gh_token_logprobs(x, t, 0, T)
+        gl, gH = torch.randn(B, device="cuda"), torch.randn(B, device="cuda")
+        want = gh.gh_token_logprobs_vjp(x, t, lse, ent, gl, gH, T)
+        check_vjp(x, t, gl, gH, T, want)
+        for _ in range(5):
+            y = x.clone()
+            gh.gh_token_logprobs_vjp(y, t, lse, ent, gl, gH, T, grad=y)
+            assert torch.equal(y, want)
+
+
+def test_backward_captured_beside_an_eager_graph(cuda_device):
+    """The functional forward and backward in a CUDA graph, replayed on new inputs,
+    while eager calls of other leaves go on."""
+    x = logits(300, 2003, torch.bfloat16, 97)
+    t = given(300, 2003, 97)
+    leaf = x.clone().requires_grad_(True)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for _ in range(2):
+            lp, ent = GF.token_logprobs(leaf, t)
+            torch.autograd.grad((lp + 0.1 * ent).sum(), leaf)
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lp, ent = GF.token_logprobs(leaf, t)
+        (grad,) = torch.autograd.grad((lp + 0.1 * ent).sum(), leaf)
+    for seed in (98, 99):
+        y = logits(300, 2003, torch.bfloat16, seed)
+        with torch.no_grad():
+            leaf.copy_(y)
+        g.replay()
+        other = y.clone().requires_grad_(True)
+        lp2, ent2 = GF.token_logprobs(other, t)
+        (lp2 + 0.1 * ent2).sum().backward()
+        torch.cuda.synchronize()
+        assert torch.equal(grad, other.grad) and torch.equal(lp, lp2)

@@ -31,6 +31,7 @@ BAD, UNSUPPORTED = gh.GH_ERR_INVALID_ARG, gh.GH_ERR_UNSUPPORTED
     (dict(lse=None), BAD), (dict(top=None), BAD), (dict(ids=None), BAD),
     (dict(logits=at(0) + 1), BAD), (dict(index=at(1) + 4), BAD), (dict(lse=at(4) + 2), BAD), (dict(ids=at(6) + 4), BAD),
     (dict(B=0, logits=None), gh.GH_OK),
+    (dict(B=1 << 31), UNSUPPORTED), (dict(B=1, V=1 << 26, ld=1 << 26), UNSUPPORTED),  # grid; a row of 128 MiB
 ])
 def test_token_logprobs_refusals(L, kw, expect):
     a = dict(logits=at(0), ld=100, index=at(1), B=16, V=100, dtype=gh.GH_BF16, T=1.0, k=5, logprob=at(2),
@@ -48,6 +49,7 @@ def test_token_logprobs_refusals(L, kw, expect):
     (dict(grad=at(0) + 64), BAD),            # partial overlap
     (dict(grad=at(0), ldg=128), BAD),        # in place with another row stride
     (dict(B=0, grad=None), gh.GH_OK),
+    (dict(B=1 << 31, V=1, ld=1, ldg=1), UNSUPPORTED),
 ])
 def test_token_logprobs_vjp_refusals(L, kw, expect):
     a = dict(logits=at(0), ld=100, index=at(1), B=16, V=100, dtype=gh.GH_F32, T=1.0, lse=at(2), entropy=at(3),
@@ -63,6 +65,7 @@ def test_token_logprobs_vjp_refusals(L, kw, expect):
     (dict(red=3), BAD), (dict(logits=None), BAD), (dict(ids=None), BAD), (dict(vals=None), BAD), (dict(loss=None), BAD),
     (dict(loss=at(4) + 2), BAD), (dict(total=at(7) + 4), BAD), (dict(row=at(5) + 1), BAD), (dict(vals=at(2) + 2), BAD),
     (dict(grad=at(0) + 64), BAD), (dict(grad=at(0), ldg=128), BAD),
+    (dict(B=1 << 31, grad=None), UNSUPPORTED),
 ])
 def test_topk_distill_refusals(L, kw, expect):
     a = dict(logits=at(0), ld=100, ids=at(1), vals=at(2), B=16, V=100, K=8, dtype=gh.GH_BF16, T=1.0, renorm=1, red=0,

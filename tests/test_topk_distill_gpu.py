@@ -262,3 +262,53 @@ def test_teacher_to_linear_student(cuda_device, reduction):
         assert np.linalg.norm(got - want) <= 1e-2 * np.linalg.norm(want)
     assert not Xg.grad[:30].any()
     assert gh.gh_get_device_status() == gh.GH_OK
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B,V", [(3, 70001), (200, 90001), (9, 300_001)])
+def test_in_place_over_a_cluster(cuda_device, dtype, B, V):
+    """Rows split over several CTAs, in place: entries and rows far from 0 are read
+    before any CTA of the row stores."""
+    x = logits(B, V, dtype, 31)
+    x[1] -= 30000.0
+    x[2] = torch.finfo(dtype).min
+    i, v = entries(x, 64, 1.0, True, 32, ragged=False)
+    loss, want = gh.gh_topk_distill(x, i, v, 1.0, True, "sum")
+    rows = slice(0, 3)
+    l3, g3 = gh.gh_topk_distill(x[rows], i[rows], v[rows], 1.0, True, "sum")
+    check_distill(x[rows], i[rows], v[rows], 1.0, True, "sum", l3, g3)
+    tol = 4e-7 * 8 + 2.0 ** -18 + 2 * torch.finfo(dtype).eps
+    assert ((want[rows].float() - g3.float()).abs() <= tol * g3.float().abs() + 1e-6).all()
+    for _ in range(5):
+        y = x.clone()
+        l2, _ = gh.gh_topk_distill(y, i, v, 1.0, True, "sum", grad=y)
+        assert torch.equal(y, want) and torch.equal(l2, loss)
+
+
+@pytest.mark.parametrize("B,K", [(1, 1), (16, 128), (17, 128), (63, 32), (64, 32), (65, 32), (64, 33)])
+def test_counts_of_small_batches(cuda_device, B, K):
+    """Both ways of counting the rows with an entry, at their border."""
+    x = logits(B, 1000, torch.float32, B)
+    i, v = entries(x, K, 1.0, True, K)
+    if B > 1:
+        i[0] = -1
+        i[B - 1, : K - 1] = -1   # only the last entry
+    n = int(((i >= 0) & (v > -math.inf)).any(1).sum())
+    assert int(gh.gh_distill_count(i, v, 1000)) == n
+    loss, grad = gh.gh_topk_distill(x, i, v)
+    check_distill(x, i, v, 1.0, True, "mean", loss, grad)
+
+
+def test_two_calls_at_once(cuda_device):
+    xs = [logits(1300, 5003, torch.bfloat16, s) for s in (41, 42)]
+    es = [entries(x, 16, 1.0, True, s) for s, x in enumerate(xs)]
+    want = [gh.gh_topk_distill(x, *e) for x, e in zip(xs, es)]
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            a = gh.gh_topk_distill(xs[0], *es[0])
+        b = gh.gh_topk_distill(xs[1], *es[1])
+        torch.cuda.synchronize()
+        for o, w in zip((a, b), want):
+            assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
