@@ -201,8 +201,9 @@ __device__ __forceinline__ float teacher_row(const DistillArgs& a, Teacher& t, i
   return sum;
 }
 
-// Gradient of a chunk's dense part: coef 2^y, y = (x - sub) c - r.
-template <typename T, bool SUB>
+// Gradient of a chunk's dense part: coef 2^y, y = (x - sub) c - r.  CONGRUENT:
+// known to be at the same offset from 16 bytes as its logits.
+template <typename T, bool SUB, bool CONGRUENT>
 __device__ __forceinline__ void dense_chunk(const uint4& q, float sub, float c, float r, float coef, uint8_t* dst,
                                             bool congruent) {
   constexpr int ES = Elem<T>::kBytes, EPC = 16 / ES;
@@ -218,7 +219,7 @@ __device__ __forceinline__ void dense_chunk(const uint4& q, float sub, float c, 
     g[j] = e.x;
     g[j + 1] = e.y;
   }
-  if (congruent) {
+  if (CONGRUENT || congruent) {
     __stcs(reinterpret_cast<uint4*>(dst), pack16<T>(g));
   } else {
 #pragma unroll
@@ -423,17 +424,22 @@ __global__ void __launch_bounds__(32 * (W + 1), 27 / (W + 1)) distill_kernel(Dis
   }
   if (!with_grad) return;
   if (e >= 0) Elem<T>::store(dst + e * ES, coef * ex2(fmaf(edge - d.sub, a.c, -d.r)));
+  // Full batches of ordinary rows know their alignment beforehand: 343 -> 332 us
+  // at 8192 x 50257; two warps per CTA gain nothing by it (33.8 -> 35.2 us at
+  // 3383 x 5056) and test it per chunk.
+  constexpr bool kKnown = W > kDistillShortWarps;
+  const bool plain = d.sub == 0.0f && (!kKnown || congruent);
   auto put = [&](const uint4 (&q)[kBatch], int at) {
     uint8_t* const p = gbase + 16 * static_cast<int64_t>(at + lane);
-    if (at + kBatchChunks <= nc && d.sub == 0.0f) {
+    if (at + kBatchChunks <= nc && plain) {
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
-        dense_chunk<T, false>(q[i], 0.0f, a.c, d.r, coef, p + 16 * kSegChunks * i, congruent);
+        dense_chunk<T, false, kKnown>(q[i], 0.0f, a.c, d.r, coef, p + 16 * kSegChunks * i, congruent);
     } else {
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
         if (at + i * kSegChunks + lane < nc)
-          dense_chunk<T, true>(q[i], d.sub, a.c, d.r, coef, p + 16 * kSegChunks * i, congruent);
+          dense_chunk<T, true, false>(q[i], d.sub, a.c, d.r, coef, p + 16 * kSegChunks * i, congruent);
     }
   };
   while (c0 < nc) {
