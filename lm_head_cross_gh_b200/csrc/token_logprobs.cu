@@ -37,13 +37,22 @@ namespace {
 // CTAs per row, whose first merges the others' sums and alternatives through
 // distributed shared memory.
 //
-// Bound by HBM for fp32 logits ([4096, 50257]: 128 us, 6.4 TB/s), by the
-// exponentials and the instructions around them for bf16 ([8192, 50257]: 150
-// us).  Measured beside it on that shape: a ring of bulk copies with consumer
-// and finalizer warps 162 us (its row ends keep one warp busy for longer than a
-// row lasts: 328 us with 20 alternatives, 196 here), two warps per CTA 152 us,
-// eight 166 us, CTAs that take over the next row through launch control 172 us
-// (it spills).
+// Bound by HBM where no alternatives are asked for: [4096, 50257] fp32 in 120
+// us (6.8 TB/s), [8192, 50257] bf16 in 128 us from a cool start (6.4 TB/s) and
+// 138 to 147 under the power cap, with the special-function unit 67% busy.  The
+// segments' maxima (41 warp instructions more a batch of 2 KiB a warp, on 176)
+// and the row's end (2,500 with 20 alternatives) bound it with alternatives, by
+// their instructions: [4096, 50257] bf16 with 32 in 94 us, [1024, 262144] with
+// 128 in 115, [4096, 50257] fp32 with 32 in 149.
+//
+// Beside an earlier form of this one that took 150 us at [8192, 50257] bf16: a
+// ring of bulk copies with consumer and finalizer warps 162 us (its row ends
+// keep one warp busy for longer than a row lasts: 328 us with 20 alternatives,
+// 196 there, 170 now), two warps per CTA 152, eight 166, CTAs that take over the
+// next row through launch control 172 (it spills).  A ring of asynchronous
+// copies per warp 146 to 149 (137 then without it); a CTA more per SM with
+// alternatives (64 registers for 72) 93.5 for 91.3 at [4096, 50257] with 32,
+// 126 for 110 at [1024, 262144] with 128.
 // ---------------------------------------------------------------------------
 
 constexpr int kLpWarps = 4;
@@ -62,8 +71,8 @@ constexpr int kCandidates = W == 1 ? 256 : 512;
 template <int W>
 constexpr int kHitChunks = W == 1 ? 192 : 256;
 
-// Segments: a warp's load, a quarter of four lanes' loads, one lane's, or one
-// logit.  The finest are for rows with few segments per alternative.
+// Segments: a warp's load (512 bytes), four lanes' (64), one lane's (16), or one
+// logit.  The finer ones are for rows with few segments per alternative.
 enum SegKind : int { kSegElement = 0, kSegChunk = 1, kSegQuad = 2, kSegWarp = 3 };
 // What a kernel keeps for alternatives: nothing, warp segments' keys, or finer ones'.
 enum TopMode : int { kTopNone = 0, kTopWarp = 1, kTopFine = 2 };
@@ -595,7 +604,7 @@ __global__ void __launch_bounds__(32 * W, kLpResident<TOP, W>) logprobs_kernel(L
 //
 // One CTA of four warps per part of a row (parts of about 32 KiB), eight on an
 // SM; the warps stream batches as the forward does.  Bound by HBM: [8192, 50257]
-// bf16 in 254 us and [1024, 128256] fp32 in 158 us, both at the copy rate.  The
+// bf16 in 247 to 257 us and [1024, 128256] fp32 in 158, both at the copy rate.  The
 // parts' size matters because the CTAs in flight then read and write one stretch
 // of memory: 16 KiB 258 / 155 us, 64 KiB 259 / 164, 128 KiB 269 / 167, and whole
 // rows as tiles of one persistent grid 303 / 167.

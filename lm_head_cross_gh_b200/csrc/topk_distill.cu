@@ -16,14 +16,15 @@
 // second reads the row again, from L2 (the rows in flight are a third of it),
 // and stores the dense part scale T Q p_j; then the last warp, which has worked
 // out the teacher's side and the loss meanwhile, stores the K elements that
-// differ.  HBM sees one read and one write of every logit (271 + 268 MB for a
-// sixth of the bf16 case below).
+// differ.  HBM sees one read and one write of every logit (240 MB read for 238
+// MB of logits at [2368, 50257] bf16).
 //
-// [8192, 50257] bf16 with 32 entries: 337 us, [1024, 262144] bf16 with 128: 229
-// us, [4096, 50257] fp32 with 32: 330 us: 4.6 to 5 TB/s of HBM traffic with the
-// special-function unit 59% (fp32 32%) and the issue slots 42% (30%) busy; the
-// second reading of every row through L2 is what a gradient from known sums (254
-// us for the bf16 case) does not have.  Warps x CTAs per SM on the bf16 and fp32
+// [8192, 50257] bf16 with 32 entries: 332 to 340 us, [1024, 262144] bf16 with
+// 128: 220 to 229, [4096, 50257] fp32 with 32: 320 to 330 (the lower figures at
+// the full clock): 4.4 to 5 TB/s of HBM traffic with the special-function unit 62%
+// (fp32 32%) and the issue slots 46% (30%) busy; the second reading of every row
+// through L2 and the wait between the passes are what a gradient from known sums
+// (247 us for the bf16 case) does not have.  Warps x CTAs per SM on the bf16 and fp32
 // cases, before the last changes: 7 x 3 343 / 317, 7 x 4 371 / 327, 9 x 3 356 /
 // 320, 15 x 2 356 / 356, 11 x 2 352 / 342, 5 x 5 393 / 371; 7 to 10 x 3 are now
 // alike.  Rows are split over a cluster from 128 KiB on: at 256 KiB the rows in
@@ -89,7 +90,7 @@ __global__ void __launch_bounds__(256) distill_count_kernel(const int64_t* __res
 }
 
 // Batches of up to this many rows and entries are counted by every CTA itself
-// instead of by a kernel before it: a launch less, 18 -> 15 us a call at [64, 1024].
+// instead of by a kernel before it: a launch less, 3 us of a call's 18 at [64, 1024].
 constexpr int kCountInside = 64;
 constexpr int64_t kCountInsideEntries = 2048;
 
