@@ -31,6 +31,7 @@ Data parallel (one process per GPU, a batch split over the ranks of a
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (gh_ce_fwd, gh_ce_fwd_bwd, gh_chunked_linear_loss, gh_distill_count, gh_linear_ce,
                gh_selective_log_softmax, gh_token_logprobs, gh_token_logprobs_vjp, gh_topk_distill)
@@ -171,11 +172,12 @@ class _TokenLogprobs(torch.autograd.Function):
         logprob, entropy = logprob.view(lead), entropy.clone().view(lead)
         if top_logprob is None:
             return logprob, entropy
-        top_logprob, top_index = top_logprob.view(*lead, -1), top_index.view(*lead, -1)
+        top_logprob, top_index = top_logprob.view(*lead, top_k), top_index.view(*lead, top_k)
         ctx.mark_non_differentiable(top_logprob, top_index)
         return logprob, entropy, top_logprob, top_index
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g_logprob, g_entropy, *unused):
         x, t, lse, entropy = ctx.saved_tensors
         shape, temperature, ignore_index = ctx.conf
@@ -209,6 +211,7 @@ class _TopkDistillation(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g):
         (grad,) = ctx.saved_tensors
         return _scaled(grad, g).reshape(ctx.shape), None, None, None, None, None

@@ -413,3 +413,25 @@ def test_backward_captured_beside_an_eager_graph(cuda_device):
         (lp2 + 0.1 * ent2).sum().backward()
         torch.cuda.synchronize()
         assert torch.equal(grad, other.grad) and torch.equal(lp, lp2)
+
+
+@pytest.mark.parametrize("shape", [(0,), (2, 0), ()])
+def test_functional_shapes_without_rows_and_of_one_row(cuda_device, shape):
+    torch.manual_seed(2)
+    x = torch.randn(*shape, 9, device="cuda", requires_grad=True)
+    t = torch.ones(shape, dtype=torch.int64, device="cuda")
+    lp, ent, top, ids = GF.token_logprobs(x, t, 3)
+    assert lp.shape == ent.shape == shape and top.shape == ids.shape == (*shape, 3)
+    (lp.sum() + ent.sum()).backward()
+    assert x.grad.shape == x.shape
+    if shape == ():
+        assert torch.allclose(lp, torch.log_softmax(x.detach(), -1)[1], atol=1e-6)
+
+
+def test_a_second_derivative_is_refused(cuda_device):
+    x = torch.randn(4, 9, device="cuda", requires_grad=True)
+    w = torch.ones(4, device="cuda", requires_grad=True)
+    lp, _ = GF.token_logprobs(x, torch.zeros(4, dtype=torch.int64, device="cuda"))
+    (g,) = torch.autograd.grad((w * lp).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.square().sum().backward()

@@ -312,3 +312,23 @@ def test_two_calls_at_once(cuda_device):
         torch.cuda.synchronize()
         for o, w in zip((a, b), want):
             assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
+
+
+@pytest.mark.parametrize("shape", [(0,), (2, 0), ()])
+def test_functional_shapes_without_rows_and_of_one_row(cuda_device, shape):
+    torch.manual_seed(2)
+    x = torch.randn(*shape, 9, device="cuda", requires_grad=True)
+    i = torch.arange(4, device="cuda").expand(*shape, 4)
+    loss = GF.topk_distillation(x, i, torch.zeros(*shape, 4, device="cuda"))
+    loss.backward()
+    assert loss.shape == () and x.grad.shape == x.shape
+    assert (loss.item() > 0.0) == (shape == ()) and torch.isfinite(loss)
+
+
+def test_linear_student_without_rows(cuda_device):
+    X = torch.empty(0, 64, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    W = torch.randn(100, 64, device="cuda").to(torch.bfloat16).requires_grad_(True)
+    loss = GF.chunked_linear_topk_distillation(X, W, torch.empty(0, 3, dtype=torch.int64, device="cuda"),
+                                               torch.empty(0, 3, device="cuda"))
+    loss.backward()
+    assert loss.item() == 0.0 and X.grad.shape == (0, 64) and not W.grad.any()
