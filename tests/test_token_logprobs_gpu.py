@@ -435,3 +435,39 @@ def test_a_second_derivative_is_refused(cuda_device):
     (g,) = torch.autograd.grad((w * lp).sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         g.square().sum().backward()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B,V", [(4, 333), (1300, 1537), (4, 70001)])
+@pytest.mark.parametrize("T", [1e-4, 1.0, 1e4])
+def test_largest_finite_logits(cuda_device, dtype, B, V, T):
+    """Rows whose n largest logits are equal and out of the others' reach, at the
+    ends of the type's range: the uniform distribution over those n, in closed
+    form (2^-20 relative for log2 and the few roundings, the gradient as for
+    rows far from zero)."""
+    big = torch.finfo(dtype).max
+    x = torch.zeros(B, V, device="cuda", dtype=dtype)
+    at = torch.tensor([V - 1, V // 2, 3], device="cuda")
+    for r, (low, high) in enumerate(((-big, big), (0.0, big), (-big, 0.0), (big, big))):
+        x[r::4] = low
+        x[r::4, at] = high
+    n = torch.full((B,), 3.0, device="cuda")
+    n[3::4] = V
+    t = torch.full((B,), V // 2, dtype=torch.int64, device="cuda")
+    lp, ent, lse, top, ids = gh.gh_token_logprobs(x, t, 3, T)
+    want = n.log()
+    assert torch.allclose(lp, -want, rtol=2.0 ** -20, atol=0)
+    assert torch.allclose(ent, want, rtol=2.0 ** -20, atol=0)
+    assert torch.allclose(top, -want[:, None].expand(B, 3), rtol=2.0 ** -20, atol=0)
+    order = torch.tensor([3, V // 2, V - 1], device="cuda").expand(B, 3).clone()
+    order[3::4] = torch.arange(3, device="cuda")
+    assert torch.equal(ids, order)
+    gl, gH = torch.full((B,), 2.0, device="cuda"), torch.full((B,), 3.0, device="cuda")
+    grad = gh.gh_token_logprobs_vjp(x, t, lse, ent, gl, gH, T).double()
+    p = torch.zeros(B, V, device="cuda", dtype=torch.float64)
+    p[:, at] = 1.0 / 3.0
+    p[3::4] = 1.0 / V
+    expect = -2.0 * p / T
+    expect[:, V // 2] += 2.0 / T
+    tol = expect.abs() * (torch.finfo(dtype).eps / 2 + 2.0 ** -18) + 3.0 * math.log(V) * 2.0 ** -19 * p / T
+    assert ((grad - expect).abs() <= tol).all()

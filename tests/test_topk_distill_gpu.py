@@ -332,3 +332,31 @@ def test_linear_student_without_rows(cuda_device):
                                                torch.empty(0, 3, device="cuda"))
     loss.backward()
     assert loss.item() == 0.0 and X.grad.shape == (0, 64) and not W.grad.any()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B,V", [(4, 333), (1300, 1537), (4, 70001)])
+@pytest.mark.parametrize("T", [1e-4, 1.0, 1e4])
+def test_largest_finite_logits(cuda_device, dtype, B, V, T):
+    """Rows whose n largest logits are equal and out of the others' reach, at the
+    ends of the type's range, and one entry of all the teacher's probability: in
+    closed form, row loss T^2 log n and gradient T (1 / n - [j = id]) (2^-20
+    relative for log2 and the few roundings, one rounding of the output)."""
+    big = torch.finfo(dtype).max
+    x = torch.zeros(B, V, device="cuda", dtype=dtype)
+    at = torch.tensor([V - 1, V // 2, 3], device="cuda")
+    for r, (low, high) in enumerate(((-big, big), (0.0, big), (-big, 0.0), (big, big))):
+        x[r::4] = low
+        x[r::4, at] = high
+    n = torch.full((B,), 3.0, device="cuda", dtype=torch.float64)
+    n[3::4] = V
+    i = torch.tensor([V // 2, -1], device="cuda").expand(B, 2).contiguous()
+    row = torch.empty(B, device="cuda")
+    _, grad = gh.gh_topk_distill(x, i, torch.zeros(B, 2, device="cuda"), T, True, "sum", row_loss=row)
+    assert torch.allclose(row.double(), T * T * n.log(), rtol=2.0 ** -19, atol=0)
+    p = torch.zeros(B, V, device="cuda", dtype=torch.float64)
+    p[:, at] = 1.0 / 3.0
+    p[3::4] = 1.0 / V
+    want = T * p
+    want[:, V // 2] -= T
+    assert ((grad.double() - want).abs() <= want.abs() * (torch.finfo(dtype).eps / 2 + 2.0 ** -19)).all()
