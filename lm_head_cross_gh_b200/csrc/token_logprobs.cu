@@ -574,8 +574,10 @@ __global__ void __launch_bounds__(32 * W, kLpResident<TOP, W>) logprobs_kernel(L
           if (lane == 0) sh.listed = got;
         }
         __syncthreads();
+        // (a row without a distribution may have too few alternatives for its places)
         const RowDist d = sh.dist;
-        const int got = sh.listed;
+        for (int i = tid; d.none && i < a.top_k; i += kThreads) write_top(a, row, d, i, 0);
+        const int got = d.none ? 0 : sh.listed;
         for (int i = tid; i < got; i += kThreads) {
           const uint64_t key = gathered[sh.list[i]];
           int above = 0;

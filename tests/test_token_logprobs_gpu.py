@@ -471,3 +471,24 @@ def test_largest_finite_logits(cuda_device, dtype, B, V, T):
     expect[:, V // 2] += 2.0 / T
     tol = expect.abs() * (torch.finfo(dtype).eps / 2 + 2.0 ** -18) + 3.0 * math.log(V) * 2.0 ** -19 * p / T
     assert ((grad - expect).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B,V", [(6, 70001), (6, 700), (1300, 1537), (1300, 20001)])
+def test_rows_of_nan_write_every_alternative(cuda_device, dtype, B, V):
+    """Rows of NaN throughout, but for three logits, or for one half: every place
+    of the given outputs is written."""
+    x = logits(B, V, dtype, 17)
+    x[0] = math.nan
+    x[1] = math.nan
+    x[1, 5:8] = 1.0
+    x[2, : V // 2] = math.nan
+    x[3, V // 2:] = math.nan
+    k = 40
+    top = torch.full((B, k), 5.0, device="cuda")
+    ids = torch.full((B, k), 5, dtype=torch.int64, device="cuda")
+    t = given(B, V, 18, 0.0)
+    lp, ent, lse, _, _ = gh.gh_token_logprobs(x, t, k, top_logprob=top, top_index=ids)
+    assert torch.isnan(torch.stack((lp[:4], ent[:4], lse[:4]))).all()
+    assert torch.isnan(top[:4]).all() and (ids[:4] == -1).all()
+    check_logprobs(x[4:], t[4:], k, 1.0, [v[4:] for v in (lp, ent, lse, top, ids)])
