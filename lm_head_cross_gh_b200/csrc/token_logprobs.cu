@@ -77,6 +77,12 @@ enum SegKind : int { kSegElement = 0, kSegChunk = 1, kSegQuad = 2, kSegWarp = 3 
 // What a kernel keeps for alternatives: nothing, warp segments' keys, or finer ones'.
 enum TopMode : int { kTopNone = 0, kTopWarp = 1, kTopFine = 2 };
 
+// How many segments may be listed for k alternatives.  A few more than k end the
+// search for a threshold sooner: [1, 50257] bf16 with 20 alternatives 10.5 -> 9.2
+// us, [214, 22627] fp32 with 36 17.4 -> 15.2; k / 4 + 4 more gain the same there,
+// but cost more ranking: [2701, 3400] fp32 with 107 31.1 -> 32.6 us.
+__host__ __device__ constexpr int most_listed(int k) { return k + k / 8 + 2; }
+
 template <int W>
 struct LpShared {
   LaneSums<W, true> sums;
@@ -84,7 +90,7 @@ struct LpShared {
   RowDist dist;
   int count, chunks, listed;
   float least;
-  int list[GH_MAX_TOP_K];
+  int list[most_listed(GH_MAX_TOP_K)];
 };
 template <int W>
 struct LpTopShared {
@@ -93,8 +99,8 @@ struct LpTopShared {
   uint4 hit[kHitChunks<W>];    // chunks with a candidate, and which they are
   int hit_chunk[kHitChunks<W>];
 };
-static_assert(kCandidates<1> >= kTopBuf && kCandidates<kLpWarps> >= kTopBuf, "the slow way's buffer");
 static_assert(kMaxSlices * GH_MAX_TOP_K <= 1024, "the keys gathered by a cluster's first CTA");
+static_assert(kCandidates<1> >= kTopBuf && kCandidates<kLpWarps> >= kTopBuf, "the slow way's buffer");
 
 // Rows that count: 1; ignored: 0; an index outside [0, V): -1.
 __device__ __forceinline__ int row_kind(const LogprobArgs& a, int64_t row) {
@@ -141,10 +147,10 @@ struct LaneKeys {
   }
   // how many of the warp's keys are >= c
   __device__ __forceinline__ int count(uint32_t c) const {
-    int n = 0;
+    int n[4] = {};  // (short chains)
 #pragma unroll
-    for (int i = 0; i < R; ++i) n += v[i] >= c ? 1 : 0;
-    return __reduce_add_sync(0xffffffffu, n);
+    for (int i = 0; i < R; ++i) n[i % 4] += v[i] >= c ? 1 : 0;
+    return __reduce_add_sync(0xffffffffu, n[0] + n[1] + (n[2] + n[3]));
   }
   __device__ __forceinline__ uint32_t lane_max() const {
     uint32_t m = 0;
@@ -201,16 +207,20 @@ struct LaneKeys<0> {
   }
 };
 
-// The k-th largest of more than k keys, by one warp, in units of 2^kShift (bf16
-// keys differ in their upper 16 bits only): bisection between the least of the
-// lanes' largest keys (32 keys reach it; stepping down from there for larger k)
-// and the largest.  It stops at a value that exactly k keys reach (*exact).
+static_assert(most_listed(GH_MAX_TOP_K) < 256, "the zeros behind the keys are never listed");
+
+// A value that k to most_listed(k) of more than k keys reach (*found), or the
+// k-th largest key where ties leave no such value, by one warp, in units of
+// 2^kShift (bf16 keys differ in their upper 16 bits only): bisection between the
+// least of the lanes' largest keys (32 keys reach it; stepping down from there
+// for larger k) and the largest.
 template <typename T, int R>
-__device__ __forceinline__ uint32_t kth_key(const LaneKeys<R>& keys, int k, bool* exact) {
+__device__ __forceinline__ uint32_t kth_key(const LaneKeys<R>& keys, int k, bool* found) {
   constexpr int kShift = Elem<T>::kBytes == 2 ? 16 : 0;
+  const int most = most_listed(k);
   const uint32_t m = keys.lane_max();
   uint32_t hi = __reduce_max_sync(0xffffffffu, m) >> kShift, lo = __reduce_min_sync(0xffffffffu, m) >> kShift;
-  *exact = false;
+  *found = false;
   if (k > 32) {
     uint32_t step = hi - lo + 1;
     int n;
@@ -219,31 +229,32 @@ __device__ __forceinline__ uint32_t kth_key(const LaneKeys<R>& keys, int k, bool
       lo = lo > step ? lo - step : 0;
       step *= 2;
     }
-    *exact = n == k;
+    *found = n <= most;
   }
-  while (lo < hi && !*exact) {
+  while (lo < hi && !*found) {
     const uint32_t mid = lo + (hi - lo + 1) / 2;
     const int n = keys.count(mid << kShift);
     if (n >= k) lo = mid;
     else hi = mid - 1;
-    *exact = n == k;
+    *found = n >= k && n <= most;
   }
   return lo << kShift;
 }
 
-// The first k segments by (key descending, position ascending) of `segs` keys
-// (padded with zeros to a multiple of 128), by one warp: their positions into
-// list[], in order; returns how many, and in thr a key that
-// k of all the logits reach (0 where there are no more than k segments).
+// Segments that hold the k largest logits, of `segs` with these keys (padded with
+// zeros to a multiple of 128), by one warp: all that reach a key that k of them
+// reach, or the first k by (key descending, position ascending).  Their
+// positions go into list[], in order; returns how many (at most most_listed(k)),
+// and in thr a key that k of all the logits reach (0: no more than k segments).
 template <typename T, int R>
 __device__ __forceinline__ int pick_from(const uint32_t* keys, int segs, int k, int* list, uint32_t* thr) {
   const int lane = static_cast<int>(threadIdx.x) & 31;
   LaneKeys<R> v;
   v.load(keys, segs);
-  bool exact;
-  const uint32_t key = kth_key<T, R>(v, k, &exact);
+  bool found;
+  const uint32_t key = kth_key<T, R>(v, k, &found);
   *thr = key;
-  if (exact) return v.list_from(key, list);
+  if (found) return v.list_from(key, list);
   // Some keys tie at the k-th: all above it, and the first of the equal ones.
   // (A negative bf16 value's key ends in ones: compare the kept bits.)
   const uint32_t mask = Elem<T>::kBytes == 2 ? 0xffff0000u : 0xffffffffu;
@@ -555,9 +566,11 @@ __global__ void __launch_bounds__(32 * W, kLpResident<TOP, W>) logprobs_kernel(L
         }
       }
       if constexpr (TOP != kTopNone) {
-        // the parts' alternatives in the row's order, then as logits of a row
-        // whose segments are single logits
+        // The parts' alternatives in the row's order, then as logits of a row whose
+        // segments are single logits; up to 64 are all ranked ([142, 167081] bf16
+        // with 4 alternatives 22.4 -> 21.0 us; 96 of them lose, 10.5 -> 10.7).
         const int total = a.slices * a.top_k;
+        const bool pick = total > 64;
         uint64_t* const gathered = reinterpret_cast<uint64_t*>(seg_keys + (total + 127) / 128 * 128);
         for (int i = tid; i < (total + 127) / 128 * 128; i += kThreads) {
           uint64_t key = 0;
@@ -568,21 +581,23 @@ __global__ void __launch_bounds__(32 * W, kLpResident<TOP, W>) logprobs_kernel(L
           seg_keys[i] = static_cast<uint32_t>(key >> 32);
         }
         __syncthreads();
-        if (warp == 0) {
-          uint32_t thr;
-          const int got = pick_segments<T>(seg_keys, total, a.top_k, sh.list, &thr);
-          if (lane == 0) sh.listed = got;
+        if (pick) {
+          if (warp == 0) {
+            uint32_t thr;
+            const int got = pick_segments<T>(seg_keys, total, a.top_k, sh.list, &thr);
+            if (lane == 0) sh.listed = got;
+          }
+          __syncthreads();
         }
-        __syncthreads();
         // (a row without a distribution may have too few alternatives for its places)
         const RowDist d = sh.dist;
         for (int i = tid; d.none && i < a.top_k; i += kThreads) write_top(a, row, d, i, 0);
-        const int got = d.none ? 0 : sh.listed;
+        const int got = d.none ? 0 : pick ? sh.listed : total;
         for (int i = tid; i < got; i += kThreads) {
-          const uint64_t key = gathered[sh.list[i]];
+          const uint64_t key = gathered[pick ? sh.list[i] : i];
           int above = 0;
-          for (int j = 0; j < got; ++j) above += gathered[sh.list[j]] > key ? 1 : 0;
-          write_top(a, row, d, above, key);
+          for (int j = 0; j < got; ++j) above += gathered[pick ? sh.list[j] : j] > key ? 1 : 0;
+          if (above < a.top_k) write_top(a, row, d, above, key);
         }
       }
     }
