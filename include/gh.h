@@ -362,7 +362,7 @@ gh_status_t gh_token_logprobs_vjp(const void* logits, int64_t ld, const int64_t*
  * A row without a distribution (see gh_token_logprobs) or with a NaN value
  * gives a NaN loss and gradient row.  An id outside [0, V) other than -1 is
  * treated as none and records GH_ERR_TARGET_RANGE.  Scratch (stream-ordered): at
- * most 5 bytes a row and 272.  GH_ERR_UNSUPPORTED where B times a
+ * most 5 bytes a row and 1040.  GH_ERR_UNSUPPORTED where B times a
  * row's CTAs (at most 8) reaches 2^31.
  *
  * gh_distill_count — count = number of rows with an entry (int64 device

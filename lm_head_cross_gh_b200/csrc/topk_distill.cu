@@ -50,7 +50,9 @@ namespace {
 constexpr int kDistillWarps = 8, kDistillShortWarps = 2;
 constexpr int64_t kDistillShortChunks = 2048;
 constexpr int kLaneEntries = GH_MAX_TOP_K / 32;
-constexpr int kCountParts = 64;  // CTAs of the counting kernel
+// CTAs of the counting kernel, its latency being a few rows' a warp ([8192, 50257]
+// 334 us a call with 64, 330 with 256; [1766, 1252] 19.3, 18.9).
+constexpr int kCountParts = 256;
 
 __device__ __forceinline__ bool distill_entry(int64_t id, float v, int64_t V) {
   return id >= 0 && id < V && !(v == kNegInf);
@@ -74,8 +76,9 @@ __global__ void __launch_bounds__(256) distill_count_kernel(const int64_t* __res
     for (int k0 = 0; k0 < K; k0 += 32) {
       const int k = k0 + lane;
       const int64_t id = k < K ? ids[row * K + k] : -1;
+      const float v = k < K ? values[row * K + k] : kNegInf;
       if (id < -1 || id >= V) record_status(GH_ERR_TARGET_RANGE);
-      const bool has = id >= 0 && distill_entry(id, values[row * K + k], V);
+      const bool has = distill_entry(id, v, V);
       any |= __any_sync(0xffffffffu, has);
     }
     n += any ? 1 : 0;
