@@ -39,16 +39,16 @@ namespace {
 //
 // Bound by HBM where no alternatives are asked for: [4096, 50257] fp32 in 120
 // us (6.8 TB/s), [8192, 50257] bf16 in 128 us from a cool start (6.4 TB/s) and
-// 138 to 147 under the power cap, with the special-function unit 67% busy.  The
+// 133 to 147 under the power cap, with the special-function unit 67% busy.  The
 // segments' maxima (41 warp instructions more a batch of 2 KiB a warp, on 176)
 // and the row's end (2,500 with 20 alternatives) bound it with alternatives, by
-// their instructions: [4096, 50257] bf16 with 32 in 94 us, [1024, 262144] with
-// 128 in 115, [4096, 50257] fp32 with 32 in 149.
+// their instructions: [4096, 50257] bf16 with 32 in 91 to 96 us, [1024, 262144]
+// with 128 in 110 to 118, [4096, 50257] fp32 with 32 in 147 to 153.
 //
 // Beside an earlier form of this one that took 150 us at [8192, 50257] bf16: a
 // ring of bulk copies with consumer and finalizer warps 162 us (its row ends
 // keep one warp busy for longer than a row lasts: 328 us with 20 alternatives,
-// 196 there, 170 now), two warps per CTA 152, eight 166, CTAs that take over the
+// 196 there, 163 to 174 now), two warps per CTA 152, eight 166, CTAs that take over the
 // next row through launch control 172 (it spills).  A ring of asynchronous
 // copies per warp 146 to 149 (137 then without it); a CTA more per SM with
 // alternatives (64 registers for 72) 93.5 for 91.3 at [4096, 50257] with 32,

@@ -19,9 +19,9 @@
 // differ.  HBM sees one read and one write of every logit (240 MB read for 238
 // MB of logits at [2368, 50257] bf16).
 //
-// [8192, 50257] bf16 with 32 entries: 332 to 340 us, [1024, 262144] bf16 with
-// 128: 220 to 229, [4096, 50257] fp32 with 32: 320 to 330 (the lower figures at
-// the full clock): 4.4 to 5 TB/s of HBM traffic with the special-function unit 62%
+// [8192, 50257] bf16 with 32 entries: 316 to 335 us, [1024, 262144] bf16 with
+// 128: 214 to 222, [4096, 50257] fp32 with 32: 312 to 326 (boards and clocks
+// differ): 4.4 to 5 TB/s of HBM traffic with the special-function unit 62%
 // (fp32 32%) and the issue slots 46% (30%) busy; the second reading of every row
 // through L2 and the wait between the passes are what a gradient from known sums
 // (247 us for the bf16 case) does not have.  Warps x CTAs per SM on the bf16 and fp32
@@ -32,7 +32,8 @@
 // exchanges cost more (424 us for the bf16 rows).  Also tried: sums and
 // gradients as items of 32 KiB handed out in an order that keeps a row in L2
 // (462 / 403 us, the items' ends), a quarter of the exponentials as polynomials
-// (355 us and more).
+// (355 us and more), each CTA finding out itself whether its row has an entry (326
+// us for 318).
 #include "ce.h"
 #include "linear_ce.h"
 #include "profile.h"
