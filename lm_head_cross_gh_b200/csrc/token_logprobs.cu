@@ -245,7 +245,7 @@ __device__ __forceinline__ uint32_t kth_key(const LaneKeys<R>& keys, int k, bool
 // zeros to a multiple of 128), by one warp: all that reach a key that k of them
 // reach, or the first k by (key descending, position ascending).  Their
 // positions go into list[], in order; returns how many (at most most_listed(k)),
-// and in thr a key that k of all the logits reach (0: no more than k segments).
+// and in thr a key that k of all the logits reach (0: all are listed).
 template <typename T, int R>
 __device__ __forceinline__ int pick_from(const uint32_t* keys, int segs, int k, int* list, uint32_t* thr) {
   const int lane = static_cast<int>(threadIdx.x) & 31;
@@ -276,7 +276,8 @@ __device__ __forceinline__ int pick_from(const uint32_t* keys, int segs, int k, 
 
 template <typename T>
 __device__ __forceinline__ int pick_segments(const uint32_t* keys, int segs, int k, int* list, uint32_t* thr) {
-  if (segs <= k) {
+  // (fewer segments than that: a key below every logit's could be found)
+  if (segs <= most_listed(k)) {
     for (int i = static_cast<int>(threadIdx.x) & 31; i < segs; i += 32) list[i] = i;
     *thr = 0;
     return segs;

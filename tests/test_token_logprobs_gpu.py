@@ -492,3 +492,23 @@ def test_rows_of_nan_write_every_alternative(cuda_device, dtype, B, V):
     assert torch.isnan(torch.stack((lp[:4], ent[:4], lse[:4]))).all()
     assert torch.isnan(top[:4]).all() and (ids[:4] == -1).all()
     check_logprobs(x[4:], t[4:], k, 1.0, [v[4:] for v in (lp, ent, lse, top, ids)])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B", [4, 1300])
+@pytest.mark.parametrize("mask", [None, -math.inf, "lowest"])
+def test_alternatives_nearly_as_many_as_logits(cuda_device, dtype, B, mask):
+    """Short rows whose alternatives are most of their logits, the ragged ends
+    among them, at every alignment and with most logits masked."""
+    for V in (9, 12, 18, 25, 73, 139, 150):
+        for k in {1, 2, V // 2, min(V - 1, 128), min(V - 5, 128), min(V, 128)}:
+            pad = (V + k) % 8
+            x = logits(B, V, dtype, V + k, pad)
+            if mask is not None:
+                x[1::2, V // 5:] = torch.finfo(dtype).min if mask == "lowest" else mask
+            t = torch.zeros(B, dtype=torch.int64, device="cuda")
+            out = gh.gh_token_logprobs(x, t, k, 0.8)
+            order = torch.sort(x.double(), dim=1, descending=True, stable=True).indices[:, :k]
+            assert torch.equal(out[4], order), f"V={V} k={k}"
+            if B < 10 and mask != "lowest":
+                check_logprobs(x, t, k, 0.8, out, what=f"V={V} k={k}")
