@@ -386,11 +386,13 @@ __global__ void __launch_bounds__(32 * (W + 1), 27 / (W + 1)) distill_kernel(Dis
     if (rank == 0) {
       float loss = 0.0f;
       for (int k = lane; k < a.K; k += 32) {
-        const float lp = d.none ? kNaN : log_p(d, t.x[k], a.temperature);
-        if (t.id[k] >= 0 && !(t.q[k] == 0.0f)) loss = fmaf(t.q[k], t.log_q[k] - lp, loss);
+        // T (log q - log p), finite also where the entry's logit is a mask's lowest value
+        const float gap = d.none ? kNaN : a.temperature * (t.log_q[k] + d.l) - (t.x[k] - d.m);
+        const float q = a.temperature * t.q[k];
+        if (t.id[k] >= 0 && !(q == 0.0f)) loss = fmaf(q, gap, loss);
       }
       loss = warp_sum(loss);
-      if (lane == 0) a.row_loss[row] = a.temperature * a.temperature * loss;
+      if (lane == 0) a.row_loss[row] = loss;
     }
     if (!with_grad) return;
     // the gradient at the entries of this CTA's part of the row: Q p less the q

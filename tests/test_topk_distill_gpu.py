@@ -360,3 +360,37 @@ def test_largest_finite_logits(cuda_device, dtype, B, V, T):
     want = T * p
     want[:, V // 2] -= T
     assert ((grad.double() - want).abs() <= want.abs() * (torch.finfo(dtype).eps / 2 + 2.0 ** -19)).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B", [4, 1300])
+@pytest.mark.parametrize("T", [0.5, 2.0])
+def test_entry_at_a_logit_of_the_lowest_value(cuda_device, dtype, B, T):
+    """The student's mask has its type's lowest value where the teacher has an
+    entry: log p is beyond fp32, the loss T q |x| is not (2^-19 relative: q's and
+    the sums' few roundings)."""
+    V = 1537
+    x = logits(B, V, dtype, 91)
+    x[:, 7] = torch.finfo(dtype).min
+    i = torch.tensor([11, 7, 30], device="cuda").expand(B, 3).contiguous()
+    v = torch.tensor([1.0, 0.2, 0.4], device="cuda").expand(B, 3).contiguous()
+    row = torch.empty(B, device="cuda")
+    loss, grad = gh.gh_topk_distill(x, i, v, T, row_loss=row)
+    r = oracle.topk_distill(f64(x), i.cpu().numpy(), f64(v), T)
+    assert np.isfinite(f64(row)).all() and (np.abs(f64(row) - r["row_loss"]) <= 2.0 ** -19 * r["row_loss"]).all()
+    assert torch.isfinite(grad).all()
+
+
+def test_entry_of_vanishing_probability_at_a_masked_logit(cuda_device):
+    """An entry whose probability is fp32's smallest, or 0, at a logit of -inf:
+    an infinite loss or none, never NaN (0 log 0 = 0)."""
+    x = logits(64, 300, torch.float32, 5)
+    x[:, 7] = -math.inf
+    i = torch.tensor([11, 7], device="cuda").expand(64, 2).contiguous()
+    v = torch.zeros(64, 2, device="cuda")
+    v[:, 1] = -torch.linspace(80, 120, 64, device="cuda")
+    for T in (0.05, 1.0, 8.0):
+        row = torch.empty(64, device="cuda")
+        _, grad = gh.gh_topk_distill(x, i, v * T, T, True, "sum", row_loss=row)
+        assert not torch.isnan(row).any() and torch.isfinite(grad).all()
+        assert torch.isposinf(row[0]) and torch.isfinite(row[-1])
