@@ -22,6 +22,7 @@
 #include <cstring>
 
 #include "profile.h"
+#include "threshold_search.h"
 #include "token_device.cuh"
 #include "token_ops.h"
 
@@ -209,36 +210,15 @@ struct LaneKeys<0> {
 
 static_assert(most_listed(GH_MAX_TOP_K) < 256, "the zeros behind the keys are never listed");
 
-// A value that k to most_listed(k) of more than k keys reach (*found), or the
-// k-th largest key where ties leave no such value, by one warp, in units of
-// 2^kShift (bf16 keys differ in their upper 16 bits only): bisection between the
-// least of the lanes' largest keys (32 keys reach it; stepping down from there
-// for larger k) and the largest.
+// search_threshold by one warp, in units of 2^kShift (bf16 keys differ in their
+// upper 16 bits only): between the least of the lanes' largest keys, which 32
+// keys reach, and the largest.
 template <typename T, int R>
 __device__ __forceinline__ uint32_t kth_key(const LaneKeys<R>& keys, int k, bool* found) {
   constexpr int kShift = Elem<T>::kBytes == 2 ? 16 : 0;
-  const int most = most_listed(k);
   const uint32_t m = keys.lane_max();
-  uint32_t hi = __reduce_max_sync(0xffffffffu, m) >> kShift, lo = __reduce_min_sync(0xffffffffu, m) >> kShift;
-  *found = false;
-  if (k > 32) {
-    uint32_t step = hi - lo + 1;
-    int n;
-    while ((n = keys.count(lo << kShift)) < k) {
-      hi = lo - 1;
-      lo = lo > step ? lo - step : 0;
-      step *= 2;
-    }
-    *found = n <= most;
-  }
-  while (lo < hi && !*found) {
-    const uint32_t mid = lo + (hi - lo + 1) / 2;
-    const int n = keys.count(mid << kShift);
-    if (n >= k) lo = mid;
-    else hi = mid - 1;
-    *found = n >= k && n <= most;
-  }
-  return lo << kShift;
+  const uint32_t hi = __reduce_max_sync(0xffffffffu, m) >> kShift, lo = __reduce_min_sync(0xffffffffu, m) >> kShift;
+  return search_threshold(lo, hi, k, most_listed(k), [&](uint32_t v) { return keys.count(v << kShift); }, found) << kShift;
 }
 
 // Segments that hold the k largest logits, of `segs` with these keys (padded with

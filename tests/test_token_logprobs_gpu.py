@@ -512,3 +512,45 @@ def test_alternatives_nearly_as_many_as_logits(cuda_device, dtype, B, mask):
             assert torch.equal(out[4], order), f"V={V} k={k}"
             if B < 10 and mask != "lowest":
                 check_logprobs(x, t, k, 0.8, out, what=f"V={V} k={k}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B", [9, 1250])
+@pytest.mark.parametrize("V,k", [(3900, 1), (3900, 8), (2053, 5), (700, 1), (300, 1), (450, 8), (250, 4), (80, 2),
+                                 (110, 12), (52, 6), (29, 4), (31, 20)])
+def test_nan_in_rows_of_few_segments(cuda_device, dtype, B, V, k):
+    """Rows with a NaN that have fewer segments than a warp has lanes, of each
+    segment kind (fp32: a warp's load, four lanes', one lane's, one logit)."""
+    x = logits(B, V, dtype, V + k)
+    bad = {0: [0], 1: [V - 1], 2: [V // 2], 3: [1, V // 3, V // 2 + 1, V - 2], 4: list(range(0, V, 2)), 5: list(range(V))}
+    for r, at in bad.items():
+        x[r, at] = math.nan
+    x[6, V // 2] = math.inf
+    t = given(B, V, V, 0.0)
+    top = torch.full((B, k), 5.0, device="cuda")
+    ids = torch.full((B, k), 5, dtype=torch.int64, device="cuda")
+    out = gh.gh_token_logprobs(x, t, k, top_logprob=top, top_index=ids)
+    for v in out[:4]:
+        assert torch.isnan(v[:7]).all()
+    assert (out[4][:7] == -1).all()
+    rows = slice(0, 64)
+    check_logprobs(x[rows], t[rows], k, 1.0, [v[rows] for v in out], what=f"V={V} k={k}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("k", [20, 33, 128])
+def test_a_cluster_of_nan_parts_and_one_plateau(cuda_device, dtype, k):
+    """One CTA's part of a row holds a plateau (more candidates than are kept) and
+    a NaN, the others nothing but NaN: places without a key beside a NaN's key."""
+    V = 70001
+    x = logits(4, V, dtype, 5)
+    for r, (a, b) in enumerate(((9000, 17000), (0, 8000), (62000, V))):
+        x[r] = math.nan
+        x[r, a:b] = 5.0
+        x[r, (a + b) // 2] = math.nan
+    t = given(4, V, 5, 0.0)
+    out = gh.gh_token_logprobs(x, t, k)
+    for v in out[:4]:
+        assert torch.isnan(v[:3]).all()
+    assert (out[4][:3] == -1).all()
+    check_logprobs(x[3:], t[3:], k, 1.0, [v[3:] for v in out])

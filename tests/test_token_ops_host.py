@@ -96,3 +96,22 @@ def test_python_binding_refuses_cpu_tensors():
         gh.gh_topk_distill(x, ids, torch.zeros(4, 2))
     with pytest.raises(ValueError):
         gh.gh_distill_count(ids, torch.zeros(4, 2), 8)
+
+
+def test_threshold_search_ends_for_every_key(tmp_path):
+    """The alternatives' search over order keys (tests/threshold_search_check.cpp):
+    a NaN's key beside lanes without a key spans the whole 32-bit range."""
+    import os
+    import shutil
+    import subprocess
+    gxx = shutil.which("g++") or shutil.which("c++")
+    if gxx is None:
+        pytest.skip("no C++ compiler")
+    here = os.path.dirname(os.path.abspath(__file__))
+    exe = str(tmp_path / "threshold_search_check")
+    build = subprocess.run([gxx, "-std=c++17", "-O2", "-Wall", "-Wextra", "-Werror",
+                            os.path.join(here, "threshold_search_check.cpp"), "-o", exe], capture_output=True, text=True)
+    assert build.returncode == 0, build.stderr
+    run = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert run.returncode == 0, run.stdout + run.stderr[:2000]
+    assert " 0 failed checks" in run.stdout
