@@ -104,6 +104,26 @@ __device__ __forceinline__ void finish_dist(RowDist& d, float s, float t, float 
   d.entropy = d.l - kLn2 * (t / s - y_m);
 }
 
+// One of `threads` threads' part of a far row's sums of 2^y and 2^y y, y = (x - m) c:
+// chains of kFarChain terms in fp32 and the chains in double.  (Terms of a row are
+// alike, and one chain of n of them is off by up to n 2^-25; 31,000 by 2e-4.)
+constexpr int kFarChain = 32;
+template <typename T, bool ENT>
+__device__ __forceinline__ void far_sums(const uint8_t* src, int64_t V, float m, float c, int thread, int threads,
+                                         double& s, double& t) {
+  s = t = 0.0;
+  for (int64_t j = thread; j < V;) {
+    float cs = 0.0f, ct = 0.0f;
+    for (int i = 0; i < kFarChain && j < V; ++i, j += threads) {
+      const float y = (Elem<T>::load(src + j * Elem<T>::kBytes) - m) * c, e = ex2(y);
+      cs += e;
+      if (ENT && e > 0.0f) ct = fmaf(e, y, ct);
+    }
+    s += static_cast<double>(cs);
+    if (ENT) t += static_cast<double>(ct);
+  }
+}
+
 // A row whose logits all lie far from 0 (lowest-value masks, tiny
 // temperatures), by one warp: the maximum, then the sums of (x - max) c.
 template <typename T>
@@ -114,19 +134,15 @@ __device__ __noinline__ RowDist far_row(const uint8_t* src, int64_t V, float c) 
   for (int64_t j = lane; j < V; j += 32) m = fmaxf(m, Elem<T>::load(src + j * ES));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float s = 0.0f, t = 0.0f;
-  for (int64_t j = lane; j < V; j += 32) {
-    const float y = (Elem<T>::load(src + j * ES) - m) * c, e = ex2(y);
-    s += e;
-    if (e > 0.0f) t = fmaf(e, y, t);
-  }
+  double s, t;
+  far_sums<T, true>(src, V, m, c, lane, 32, s, t);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     s += __shfl_xor_sync(0xffffffffu, s, o);
     t += __shfl_xor_sync(0xffffffffu, t, o);
   }
-  RowDist d{m, 0.0f, m, 0.0f, s, 0.0f, false};
-  finish_dist(d, s, t, 0.0f);
+  RowDist d{m, 0.0f, m, 0.0f, static_cast<float>(s), 0.0f, false};
+  finish_dist(d, d.s, static_cast<float>(t), 0.0f);
   return d;
 }
 

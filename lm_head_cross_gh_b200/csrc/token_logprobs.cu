@@ -714,11 +714,12 @@ __global__ void __launch_bounds__(kLpVjpThreads, 8) logprobs_vjp_kernel(LogprobV
   if (far) {
     // the row's first part takes it whole (in place, its sums come before any store)
     if (part != 0) return;
-    float m = kNegInf, s = 0.0f;
+    float m = kNegInf;
     for (int64_t j = tid; j < a.V; j += kLpVjpThreads) m = fmaxf(m, Elem<T>::load(r.src + j * ES));
     m = block_max<kLpVjpThreads>(m, red[0]);
-    for (int64_t j = tid; j < a.V; j += kLpVjpThreads) s += ex2((Elem<T>::load(r.src + j * ES) - m) * a.c);
-    w.hi = log2f(block_sum<kLpVjpThreads>(s, red[1]));
+    double s, unused;
+    far_sums<T, false>(r.src, a.V, m, a.c, tid, kLpVjpThreads, s, unused);
+    w.hi = log2f(block_sum<kLpVjpThreads>(static_cast<float>(s), red[1]));
     w.sub = m;
     lo = 0.0f;
     __syncthreads();

@@ -554,3 +554,35 @@ def test_a_cluster_of_nan_parts_and_one_plateau(cuda_device, dtype, k):
         assert torch.isnan(v[:3]).all()
     assert (out[4][:3] == -1).all()
     check_logprobs(x[3:], t[3:], k, 1.0, [v[3:] for v in out])
+
+
+@pytest.mark.parametrize("B,V", [(3, 70001), (1100, 20011), (3, 1_000_003)])
+@pytest.mark.parametrize("at", [-2000.0, -2e6])
+def test_long_rows_far_from_zero(cuda_device, at, B, V):
+    """Rows far from 0 whose logits have three values one nat apart: their sums
+    hold for any length, in the gradient (at -2000) and in the log-probabilities
+    too (at -2e6).  Exponentials are off by |y| 2^-23 <= 3 2^-23 and 2^-22 of ex2, a
+    chain of 32 terms by 31 2^-25 < 2^-20 and the rest of the sums by a few 2^-24:
+    together below 2^-19 for the sum and p; the entropy has that twice, and log p and
+    the entropy 2^-22 of themselves."""
+    x = at + torch.arange(V, device="cuda").remainder(3).float().expand(B, V).contiguous()
+    t = torch.arange(B, device="cuda") * 7
+    lp, ent, lse, top, ids = gh.gh_token_logprobs(x, t, 3)
+    logp = torch.log_softmax(x[0].double() - at, 0)
+    p, H = logp.exp(), -(logp.exp() * logp).sum()
+    assert ((lp.double() - logp[t]).abs() <= 2.0 ** -19 + 2.0 ** -22 * logp[t].abs()).all()
+    assert ((ent.double() - H).abs() <= 2.0 ** -18 + 2.0 ** -22 * H).all()
+    assert (ids == torch.tensor([2, 5, 8], device="cuda")).all()
+    assert ((top.double() - logp[2]).abs() <= 2.0 ** -19 + 2.0 ** -22 * logp[2].abs()).all()
+    g = gh.gh_token_logprobs_vjp(x, t, lse, ent, torch.ones(B, device="cuda"))
+    for r in range(min(B, 3)):
+        want = -p
+        want[t[r]] += 1.0
+        assert ((g[r].double() - want).abs() <= 2.0 ** -19 * p + 2.0 ** -22 * want.abs()).all()
+    q, loss = torch.zeros(B, 1, device="cuda"), torch.empty(B, device="cuda")
+    _, g = gh.gh_topk_distill(x, t[:, None].contiguous(), q, 1.0, True, "sum", row_loss=loss)
+    assert ((loss.double() + logp[t]).abs() <= 2.0 ** -19 + 2.0 ** -21 * logp[t].abs()).all()
+    for r in range(min(B, 3)):
+        want = p.clone()
+        want[t[r]] -= 1.0
+        assert ((g[r].double() - want).abs() <= 2.0 ** -19 * p + 2.0 ** -22 * want.abs()).all()
