@@ -51,10 +51,14 @@ __device__ __forceinline__ int64_t edge_element(const RowGeo& r, int64_t V, int 
 // With c = log2(e) / T and y_j = x_j c - R:  s = sum 2^y_j,  t = sum 2^y_j y_j,
 // and m the largest x.  R is m c rounded; y_j is one fused multiply-add, so R's
 // rounding moves all terms alike.  That holds while |R| <= kFarRef (R's rounding
-// is then at most 2^-5); a state with a larger R carries s = 0, and a row whose
-// largest R is one is summed again from differences to its maximum (far_row).
+// is then at most 2^-5); what comes while a state has a larger R is not summed,
+// and a row whose largest R is one is summed again from differences to its
+// maximum (far_row).  So is a row whose largest R is less than kFarSlack above
+// -kFarRef: the terms left out below that limit could count in it, while in any
+// other row they are at most 2^-kFarSlack of the largest.
 // R = +inf marks a NaN or +inf logit.
 constexpr float kFarRef = 1048576.0f;
+constexpr float kFarSlack = 256.0f;  // beyond the 2^-126 where fp32 terms end
 
 struct SoftState {
   float m, r, s, t;
@@ -150,7 +154,7 @@ __device__ __noinline__ RowDist far_row(const uint8_t* src, int64_t V, float c) 
 template <typename T>
 __device__ __forceinline__ RowDist row_dist(const SoftState& st, const uint8_t* src, int64_t V, float c) {
   if (st.r == kPosInf || st.r == kNegInf) return {0.0f, 0.0f, 0.0f, 0.0f, 1.0f, 0.0f, true};
-  if (fabsf(st.r) > kFarRef) return far_row<T>(src, V, c);
+  if (st.r > kFarRef || st.r < kFarSlack - kFarRef) return far_row<T>(src, V, c);
   RowDist d{st.m, 0.0f, 0.0f, st.r, st.s, 0.0f, false};
   finish_dist(d, st.s, st.t, fmaf(st.m, c, -st.r));
   return d;

@@ -8,7 +8,7 @@ import torch
 
 import lm_head_cross_gh_b200 as gh
 from lm_head_cross_gh_b200 import functional as GF
-from token_ops_check import check_logprobs, check_vjp, logits
+from token_ops_check import STRADDLE, check_logprobs, check_vjp, logits, straddling_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -586,3 +586,27 @@ def test_long_rows_far_from_zero(cuda_device, at, B, V):
         want = p.clone()
         want[t[r]] -= 1.0
         assert ((g[r].double() - want).abs() <= 2.0 ** -19 * p + 2.0 ** -22 * want.abs()).all()
+
+
+@pytest.mark.parametrize("B,V,k", [(9, 30, 3), (9, 2050, 5), (1250, 2050, 5), (1250, 5003, 20), (9, 16001, 0), (9, 70001, 20)])
+@pytest.mark.parametrize("T", [1.0, 1e-4])
+def test_rows_on_both_sides_of_the_far_limit(cuda_device, T, B, V, k):
+    x = straddling_rows(B, V, T, V)
+    t = given(B, V, V, 0.0)
+    t[::2] = V // 2
+    T = float(torch.tensor(T))
+    lp, ent, lse, top, ids = gh.gh_token_logprobs(x, t, k, T)
+    z = x.double() / T
+    z = z - z.amax(1, keepdim=True)
+    logp = torch.log_softmax(z, 1)
+    want = logp.gather(1, t[:, None])[:, 0]
+    H = -(logp.exp() * logp).sum(1)
+    assert ((lp.double() - want).abs() <= STRADDLE + 2.0 ** -22 * want.abs()).all()
+    assert ((ent.double() - H).abs() <= STRADDLE * (2 + 2 * H)).all()
+    w = torch.logsumexp(x.double() / T, 1)
+    assert ((lse.double() - w).abs() <= 2.0 ** -22 * w.abs()).all()
+    if k:
+        order = torch.sort(x, dim=1, descending=True, stable=True).indices[:, :k]
+        assert torch.equal(ids, order)
+        want = logp.gather(1, order)
+        assert ((top.double() - want).abs() <= STRADDLE + 2.0 ** -22 * want.abs()).all()

@@ -10,7 +10,7 @@ import torch
 import lm_head_cross_gh_b200 as gh
 import oracle
 from lm_head_cross_gh_b200 import functional as GF
-from token_ops_check import check_distill, f64, logits
+from token_ops_check import STRADDLE, check_distill, f64, logits, straddling_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -394,3 +394,27 @@ def test_entry_of_vanishing_probability_at_a_masked_logit(cuda_device):
         _, grad = gh.gh_topk_distill(x, i, v * T, T, True, "sum", row_loss=row)
         assert not torch.isnan(row).any() and torch.isfinite(grad).all()
         assert torch.isposinf(row[0]) and torch.isfinite(row[-1])
+
+
+@pytest.mark.parametrize("B,V", [(9, 30), (9, 2050), (1250, 2050), (1250, 5003), (9, 70001), (500, 40001)])
+@pytest.mark.parametrize("T", [1.0, 1e-4])
+def test_rows_on_both_sides_of_the_far_limit(cuda_device, T, B, V):
+    x = straddling_rows(B, V, T, V)
+    T = float(torch.tensor(T))
+    i = torch.tensor([0, V // 2, V - 1], device="cuda").expand(B, 3).contiguous()
+    v = T * torch.tensor([1.0, 0.5, -0.25], device="cuda").expand(B, 3).contiguous()
+    row = torch.empty(B, device="cuda")
+    _, grad = gh.gh_topk_distill(x, i, v, T, True, "sum", row_loss=row)
+    z = x.double() / T
+    logp = torch.log_softmax(z - z.amax(1, keepdim=True), 1)
+    log_q = torch.log_softmax(v.double() / T, 1)
+    q, log_p = log_q.exp(), logp.gather(1, i)
+    want = T * T * (q * (log_q - log_p)).sum(1)
+    # the log-probabilities' bound for log p and p; q's few roundings as 2^-19
+    tol = T * T * (STRADDLE + 2.0 ** -19 * (q * (log_q.abs() + log_p.abs() + 1)).sum(1))
+    assert ((row.double() - want).abs() <= tol).all()
+    want = T * logp.exp()
+    tol = STRADDLE * want
+    want.scatter_add_(1, i, -T * q)
+    tol.scatter_add_(1, i, T * q * 2.0 ** -19)
+    assert ((grad.double() - want).abs() <= tol + 2.0 ** -22 * want.abs()).all()

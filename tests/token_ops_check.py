@@ -119,3 +119,32 @@ def check_distill(x, ids, values, T, renorm, reduction, loss, grad, row_loss=Non
     assert abs(loss.item() - r["loss"]) <= scale * row_tol.sum() + 2.0 ** -22 * abs(r["loss"]), what + " loss"
     if grad is not None:
         close(f64(grad), r["grad"], tol + OUT_EPS[x.dtype] * np.abs(r["grad"]) + TINY, what + " grad")
+
+
+def straddling_rows(B, V, T, seed):
+    """fp32 rows whose logits times log2(e) / T lie on both sides of -2^20, where
+    sums relative to 0 end: the lower ones just below it, the higher ones just
+    above, in places that fall to other batches, warps and CTAs of a row.  Equal
+    steps of 1 nat (T = 1) or 3 (T = 1e-4), at most 6 of them in a row."""
+    low, high = (-726818.0, -726817.0) if T == 1.0 else (-72.6820, -72.6817)
+    x = torch.full((B, V), low, device="cuda")
+    x[0, V - 10:] = high           # the lower ones first
+    x[1, :10] = high               # the higher ones first
+    x[2, V // 2] = high
+    x[3, 3 * V // 4:] = high
+    x[4, ::777] = high
+    x[5] = high                    # none below
+    x[6, V // 3:] = high - 3 * (high - low)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    x[7:] = low + (high - low) * torch.randint(-3, 4, (B - 7, V), generator=g, device="cuda").float()
+    return x
+
+
+# The bound for these rows: a logit times c is one fused multiply-add from its
+# row's reference, or a product of its exact distance to the row's maximum, so
+# that neither's size matters: y is off by |y| 2^-23 for c's rounding and its own,
+# |y| <= 27 (18 nats and the reference's rounding), which 2^y has as 27 ln 2 2^-23
+# < 2^-18.7 relative; with 2^-22 of ex2, 2^-20 of the sums and a few roundings of
+# 2^-24 that is below 2^-17 for p, log p and the entropy's p (log p + H).
+STRADDLE = 2.0 ** -17
