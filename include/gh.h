@@ -377,6 +377,21 @@ gh_status_t gh_distill_count(const int64_t* teacher_index, const float* teacher_
                              int64_t V, int64_t* count, void* stream);
 
 /*
+ * gh_scale_grad — out = grad * g for a stored gradient and the scalar upstream
+ * gradient g of its loss: the product in fp32, rounded to `dtype` once (round to
+ * nearest even).  The autograd forms' backward.
+ *   grad     [B, V] of `dtype`, device, rows `ld` elements apart (ld >= V).
+ *   g        device float32 scalar, read by the kernel.
+ *   out      [B, V] of `dtype`, rows ld_out apart, device, written (columns from
+ *            V on are left).  out == grad with ld_out == ld is allowed (in
+ *            place); no other overlap.
+ * B >= 0, V >= 1.  No scratch.  GH_ERR_UNSUPPORTED where B times a row's parts of
+ * 32 KiB reaches 2^31.
+ */
+gh_status_t gh_scale_grad(const void* grad, int64_t ld, int64_t B, int64_t V, gh_dtype_t dtype, const float* g,
+                          void* out, int64_t ld_out, void* stream);
+
+/*
  * gh_linear_ce — chunked fused linear cross-entropy (Greyhound
  * `chunked_linear_cross_entropy` over `chunked_linear_loss`).
  *

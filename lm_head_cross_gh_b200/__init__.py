@@ -110,6 +110,8 @@ def lib() -> ctypes.CDLL:
     L.gh_topk_distill.restype = c_int
     L.gh_distill_count.argtypes = [c_void_p, c_void_p, c_int64, c_int64, c_int64, c_void_p, c_void_p]
     L.gh_distill_count.restype = c_int
+    L.gh_scale_grad.argtypes = [c_void_p, c_int64, c_int64, c_int64, c_int, c_void_p, c_void_p, c_int64, c_void_p]
+    L.gh_scale_grad.restype = c_int
     L.gh_linear_ce.argtypes = [c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int64, c_int64, c_int,
                                c_int64, c_int, c_float, c_void_p, c_void_p, c_void_p, c_void_p]
     L.gh_linear_ce.restype = c_int
@@ -709,6 +711,34 @@ def gh_topk_distill(logits, teacher_index, teacher_logits, temperature: float = 
     return loss, grad
 
 
+def gh_scale_grad(grad, g, *, out=None, stream=None):
+    """``grad * g`` for a stored gradient and the scalar upstream gradient ``g`` (CUDA
+    float32), the product in float32 and rounded once (one call into
+    ``gh_scale_grad``).
+
+    ``grad`` CUDA float32 or bfloat16, contiguous of any shape or [B, V] with dense
+    rows; ``out`` (optional output, may be ``grad`` itself) is laid out as
+    ``grad`` when not given.  Returns ``out``.
+    """
+    import torch
+    _need(grad.is_cuda, "grad: CUDA")
+    dev = grad.device
+    _need(g.dtype == torch.float32 and g.numel() == 1 and g.device == dev, "g: float32 scalar on grad's device")
+    _need(out is None or (out.shape == grad.shape and out.dtype == grad.dtype and out.device == dev), "out mismatch")
+    if grad.is_contiguous() and (out is None or out.is_contiguous()):
+        _need(grad.dtype in (torch.float32, torch.bfloat16), "grad dtype must be float32 or bfloat16")
+        out = torch.empty_like(grad) if out is None else out
+        dtype = GH_F32 if grad.dtype == torch.float32 else GH_BF16
+        B, V = (1, grad.numel()) if grad.numel() else (0, 1)
+        ld = ldo = V
+    else:
+        B, V, ld, dtype = _rows(grad, torch)
+        out, ldo = _grad_like(out, grad, B, V, ld, torch)
+    _launch("gh_scale_grad", dev, torch,
+            (grad.data_ptr(), ld, B, V, dtype, g.data_ptr(), out.data_ptr(), ldo), stream)
+    return out
+
+
 def gh_linear_ce(inputs, weight, targets, ignore_index: int = -100, reduction: str = "mean",
                  z_loss: float = 0.0, chunk: int = 0, accum: str = "fp32", *, grad_inputs=None,
                  grad_weight=None, loss=None, stream=None):
@@ -795,7 +825,7 @@ __all__ = [
     "GhError", "lib", "header_symbols", "status_string", "gh_status_string", "gh_version",
     "gh_ce_fwd_bwd", "gh_ce_fwd_bwd_noalloc", "GH_NOALLOC_MAX_ROWS", "gh_ce_fwd", "gh_selective_log_softmax",
     "gh_ce_vjp", "gh_linear_ce", "gh_chunked_linear_loss", "CHUNK_LOSS_FN",
-    "gh_token_logprobs", "gh_token_logprobs_vjp", "gh_topk_distill", "gh_distill_count", "GH_MAX_TOP_K",
+    "gh_token_logprobs", "gh_token_logprobs_vjp", "gh_topk_distill", "gh_distill_count", "gh_scale_grad", "GH_MAX_TOP_K",
     "gh_count_valid", "gh_ce_fwd_bwd_shard", "gh_linear_ce_shard", "gh_linear_ce_shard_f32",
     "gh_cast_f32_to_bf16", "gh_exp2_eval",
     "gh_get_device_status", "gh_profile_enable", "gh_profile_read", "gh_debug_set", "GH_DEBUG",

@@ -366,6 +366,29 @@ gh_status_t gh_topk_distill(const void* logits, int64_t ld, const int64_t* teach
   return distill_launch(a, dtype, loss, stream);
 }
 
+gh_status_t gh_scale_grad(const void* grad, int64_t ld, int64_t B, int64_t V, gh_dtype_t dtype, const float* g,
+                          void* out, int64_t ld_out, void* stream) {
+  if (B < 0 || V < 1 || ld < V || ld_out < V) return GH_ERR_INVALID_ARG;
+  if (dtype != GH_F32 && dtype != GH_BF16) return GH_ERR_INVALID_ARG;
+  if (B > 0 && (!grad || !g || !out)) return GH_ERR_INVALID_ARG;
+  const int es = dtype == GH_F32 ? 4 : 2;
+  if (misaligned(grad, es) || misaligned(out, es) || misaligned(g, 4)) return GH_ERR_INVALID_ARG;
+  if (B == 0) return GH_OK;
+  // (element offsets stay far inside 64 bits)
+  constexpr int64_t kMost = int64_t(1) << 56;
+  if (ld > kMost / B || ld_out > kMost / B) return GH_ERR_UNSUPPORTED;
+  if (aliases_partly(grad, ld, out, ld_out, B, V, es)) return GH_ERR_INVALID_ARG;
+  ScaleArgs a{};
+  a.grad = grad;
+  a.out = out;
+  a.g = g;
+  a.B = B;
+  a.V = V;
+  a.ld = ld;
+  a.ld_out = ld_out;
+  return scale_grad_launch(a, dtype, static_cast<cudaStream_t>(stream));
+}
+
 static gh_status_t linear_ce_impl(const void* inputs, const void* weight, const int64_t* targets, int64_t N,
                                   int64_t D, int64_t V, int64_t chunk, gh_accum_t accum_dtype, int64_t ignore_index,
                                   gh_reduction_t reduction, float z_mult, const int64_t* n_total, float* loss,

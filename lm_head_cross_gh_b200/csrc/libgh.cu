@@ -5,6 +5,7 @@
 #include "ce_vjp.cu"
 #include "token_logprobs.cu"
 #include "topk_distill.cu"
+#include "scale_grad.cu"
 #include "linear_ce.cu"
 #include "api.cu"
 #include "noalloc.cu"

@@ -1,5 +1,6 @@
-// Internal interface of the token log-probability kernels (token_logprobs.cu)
-// and the top-logits distillation kernels (topk_distill.cu).
+// Internal interface of the token log-probability kernels (token_logprobs.cu),
+// the top-logits distillation kernels (topk_distill.cu) and the stored gradients'
+// scaling (scale_grad.cu).
 #pragma once
 
 #include <cstdint>
@@ -64,6 +65,16 @@ struct DistillArgs {
   int64_t slice_chunks;       // 16-byte chunks per CTA of a row
 };
 
+struct ScaleArgs {
+  const void* grad;  // [B, V], row stride ld
+  void* out;         // [B, V], row stride ld_out (may be grad with the same stride)
+  const float* g;    // device scalar
+  int64_t B, V, ld, ld_out;
+  // set by scale_grad_launch
+  int parts;            // CTAs per row
+  int64_t part_chunks;  // 16-byte chunks each
+};
+
 gh_status_t logprobs_launch(const LogprobArgs& a, gh_dtype_t dtype, cudaStream_t stream);
 gh_status_t logprobs_vjp_launch(const LogprobVjpArgs& a, gh_dtype_t dtype, cudaStream_t stream);
 // Counts the rows with an entry into *count (written, not added to).
@@ -71,5 +82,6 @@ gh_status_t distill_count_launch(const int64_t* ids, const float* values, int64_
                                  unsigned long long* count, cudaStream_t stream);
 // Writes the scalar loss, the row losses and, with a.grad, the gradient.
 gh_status_t distill_launch(const DistillArgs& a, gh_dtype_t dtype, float* loss, cudaStream_t stream);
+gh_status_t scale_grad_launch(const ScaleArgs& a, gh_dtype_t dtype, cudaStream_t stream);
 
 }  // namespace gh

@@ -34,7 +34,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import (gh_ce_fwd, gh_ce_fwd_bwd, gh_chunked_linear_loss, gh_distill_count, gh_linear_ce,
-               gh_selective_log_softmax, gh_token_logprobs, gh_token_logprobs_vjp, gh_topk_distill)
+               gh_scale_grad, gh_selective_log_softmax, gh_token_logprobs, gh_token_logprobs_vjp, gh_topk_distill)
 
 _PKG = __name__.rpartition(".")[0]
 
@@ -45,14 +45,19 @@ __all__ = ["cross_entropy", "chunked_linear_cross_entropy", "chunked_linear_loss
 
 
 def _scaled(grad, g):
-    """grad * g for the scalar upstream gradient g.
+    """grad * g for the scalar upstream gradient g, the product in float32 and
+    rounded once (g itself rounded to a bf16 gradient's type would scale every
+    element wrongly, by up to 2^-8).
 
     The product is always formed on the device: testing ``g == 1`` first would
     read g back to the host, which stalls the stream on every backward and is
     not allowed while a CUDA graph is being captured."""
     if grad is None:
         return None
-    return grad * g.to(grad.dtype)
+    if not grad.is_cuda or (g.requires_grad and torch.is_grad_enabled()):  # (g may be differentiated further)
+        wide = torch.promote_types(grad.dtype, torch.float32)
+        return (grad.to(wide) * g.to(wide)).to(grad.dtype)
+    return gh_scale_grad(grad, g.float())
 
 
 class _CrossEntropy(torch.autograd.Function):

@@ -115,3 +115,31 @@ def test_threshold_search_ends_for_every_key(tmp_path):
     run = subprocess.run([exe], capture_output=True, text=True, timeout=120)
     assert run.returncode == 0, run.stdout + run.stderr[:2000]
     assert " 0 failed checks" in run.stdout
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(B=-1), BAD), (dict(V=0), BAD), (dict(ld=98), BAD), (dict(ldo=98), BAD), (dict(dtype=2), BAD),
+    (dict(grad=None), BAD), (dict(g=None), BAD), (dict(out=None), BAD), (dict(grad=at(0) + 1), BAD),
+    (dict(out=at(2) + 1), BAD), (dict(g=at(1) + 2), BAD),
+    (dict(out=at(0) + 64), BAD),           # partial overlap
+    (dict(out=at(0), ldo=128), BAD),       # in place with another row stride
+    (dict(B=0, grad=None, g=None, out=None), gh.GH_OK),
+    (dict(B=1 << 31), UNSUPPORTED), (dict(B=1 << 40, ld=1 << 40), UNSUPPORTED),
+])
+def test_scale_grad_refusals(L, kw, expect):
+    a = dict(grad=at(0), ld=100, B=16, V=99, dtype=gh.GH_BF16, g=at(1), out=at(100), ldo=100)
+    a.update(kw)
+    assert L.gh_scale_grad(a["grad"], a["ld"], a["B"], a["V"], a["dtype"], a["g"], a["out"], a["ldo"], None) == expect
+
+
+def test_a_bf16_gradient_is_scaled_by_the_unrounded_upstream_gradient():
+    from lm_head_cross_gh_b200 import functional as GF
+    torch.manual_seed(0)
+    x = torch.randn(64, 100).to(torch.bfloat16)
+    for g in (0.3, 1.0 / 3.0, -1.37):
+        got = GF._scaled(x, torch.tensor(g))
+        assert torch.equal(got, (x.float() * g).to(torch.bfloat16))
+        # over many elements the roundings' mean is far below g's own in bf16 (0.1 to 0.3%):
+        # 6400 of at most 2^-8 each, 2^-8 / 80 as a random walk, bounded at 5 of those
+        ratio = float((got.double() * x.double()).sum() / (x.double() ** 2).sum()) / float(torch.tensor(g))
+        assert abs(ratio - 1.0) <= 5 * 2.0 ** -8 / 80
