@@ -30,6 +30,8 @@ Data parallel (one process per GPU, a batch split over the ranks of a
 """
 from __future__ import annotations
 
+import math
+
 import torch
 from torch.autograd.function import once_differentiable
 
@@ -165,11 +167,26 @@ def _dense_rows(logits):
     return x
 
 
+def _rows_of(t, name, lead, *tail):
+    """A companion of logits [*lead, V] as [rows, *tail], row by row: it has the
+    logits' leading shape, or is flat already (dimensions of 1 apart).  Any other
+    shape of as many elements would pair the wrong rows."""
+    rows, n = math.prod(lead), t.dim() - len(tail)
+
+    def ones_dropped(shape):
+        return [d for d in shape if d != 1]
+
+    if (n < 0 or tuple(t.shape[n:]) != tail
+            or ones_dropped(t.shape[:n]) not in (ones_dropped(lead), ones_dropped((rows,)))):
+        raise ValueError(f"{name}: shape {[*lead, *tail]} or {[rows, *tail]}, not {list(t.shape)}")
+    return t.reshape(rows, *tail).contiguous()
+
+
 class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, index, top_k, temperature, ignore_index):
         x = _dense_rows(logits)
-        t = index.reshape(-1).contiguous()
+        t = _rows_of(index, "index", logits.shape[:-1])
         logprob, entropy, lse, top_logprob, top_index = gh_token_logprobs(x, t, top_k, temperature, ignore_index)
         ctx.save_for_backward(x, t, lse, entropy)
         ctx.conf = (logits.shape, temperature, ignore_index)
@@ -192,9 +209,9 @@ class _TokenLogprobs(torch.autograd.Function):
 
 
 def token_logprobs(logits, index, top_k: int = 0, temperature: float = 1.0, ignore_index: int = -100):
-    """Log-probabilities of ``index`` [...] under ``logits`` [..., V] (float32 or
-    bfloat16, CUDA) over ``temperature``, and the rows' entropies: float32 [...]
-    each, both differentiable.  With ``top_k`` also the most probable
+    """Log-probabilities of ``index`` [...] (or flat) under ``logits`` [..., V]
+    (float32 or bfloat16, CUDA) over ``temperature``, and the rows' entropies:
+    float32 [...] each, both differentiable.  With ``top_k`` also the most probable
     alternatives' log-probabilities (float32) and ids (int64) [..., top_k], which
     carry no gradient.  Rows whose index is ``ignore_index`` give 0, 0, -inf and
     -1 and a zero gradient."""
@@ -205,9 +222,9 @@ class _TopkDistillation(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, teacher_index, teacher_logits, temperature, renormalize, reduction):
         x = _dense_rows(logits)
-        K = teacher_index.shape[-1]
-        ids = teacher_index.reshape(-1, K).contiguous()
-        values = teacher_logits.reshape(-1, K).float().contiguous()
+        lead, K = logits.shape[:-1], teacher_index.shape[-1]
+        ids = _rows_of(teacher_index, "teacher_index", lead, K)
+        values = _rows_of(teacher_logits.float(), "teacher_logits", lead, K)
         ctx.shape = logits.shape
         loss, grad = gh_topk_distill(x, ids, values, temperature, renormalize, reduction,
                                      with_grad=ctx.needs_input_grad[0])
@@ -226,7 +243,7 @@ def topk_distillation(logits, teacher_index, teacher_logits, temperature: float 
                       reduction: str = "mean"):
     """Distillation of ``logits`` [..., V] (float32 or bfloat16, CUDA) from a
     teacher's stored entries ``teacher_index`` (int64) and ``teacher_logits``
-    [..., K]: ``temperature**2`` times the Kullback-Leibler sum over the entries
+    [..., K] (or flat, [rows, K]): ``temperature**2`` times the Kullback-Leibler sum over the entries
     (see ``gh_topk_distill``).  Returns a float32 scalar; its backward gives the
     logits gradient computed in the forward pass (the teacher gets none)."""
     return _TopkDistillation.apply(logits, teacher_index, teacher_logits, float(temperature), bool(renormalize),
@@ -241,8 +258,9 @@ def chunked_linear_topk_distillation(inputs, weight, teacher_index, teacher_logi
     with the distillation in place on each chunk): ``teacher_index`` and
     ``teacher_logits`` are [BT, K]; a mean divides by all chunks' rows with an
     entry.  The chunk logits are bf16, as for any ``chunked_linear_loss``."""
-    ids = teacher_index.contiguous()
-    values = teacher_logits.float().contiguous()
+    lead, K = inputs.shape[:-1], teacher_index.shape[-1]
+    ids = _rows_of(teacher_index, "teacher_index", lead, K)
+    values = _rows_of(teacher_logits.float(), "teacher_logits", lead, K)
     total = gh_distill_count(ids, values, weight.shape[0])
 
     def loss_and_grad(logits, ids, values):

@@ -610,3 +610,15 @@ def test_rows_on_both_sides_of_the_far_limit(cuda_device, T, B, V, k):
         assert torch.equal(ids, order)
         want = logp.gather(1, order)
         assert ((top.double() - want).abs() <= STRADDLE + 2.0 ** -22 * want.abs()).all()
+
+
+def test_functional_companions_may_be_flat(cuda_device):
+    x = logits(12, 77, torch.float32, 3).view(3, 4, 77)
+    t = given(12, 77, 3)
+    a, b = GF.token_logprobs(x, t, 5), GF.token_logprobs(x, t.view(3, 4), 5)
+    assert all(torch.equal(p, q) for p, q in zip(a, b)) and a[0].shape == (3, 4)
+    assert torch.equal(GF.token_logprobs(x, t.view(3, 4, 1), 5)[0], a[0])
+    ids, top = a[3], a[2]
+    l1 = GF.topk_distillation(x, ids, top, 2.0)
+    l2 = GF.topk_distillation(x, ids.reshape(12, 5), top.reshape(12, 5), 2.0)
+    assert torch.equal(l1, l2)

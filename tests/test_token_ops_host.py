@@ -143,3 +143,24 @@ def test_a_bf16_gradient_is_scaled_by_the_unrounded_upstream_gradient():
         # 6400 of at most 2^-8 each, 2^-8 / 80 as a random walk, bounded at 5 of those
         ratio = float((got.double() * x.double()).sum() / (x.double() ** 2).sum()) / float(torch.tensor(g))
         assert abs(ratio - 1.0) <= 5 * 2.0 ** -8 / 80
+
+
+def test_functional_forms_refuse_companions_of_another_shape():
+    """Rows of an index, ids or values of another shape than the logits' would be
+    paired wrongly, whatever their number."""
+    from lm_head_cross_gh_b200 import functional as GF
+    x, i, v = torch.zeros(2, 6, 9), torch.zeros(2, 6, 3, dtype=torch.int64), torch.zeros(2, 6, 3)
+    for index in (i[..., 0].t(), i[0, :, 0], i.reshape(4, 9), i[..., :2], i[:1, :, 0], i[0, 0, 0]):
+        with pytest.raises(ValueError, match="index"):
+            GF.token_logprobs(x, index)
+    for ids, values, name in ((i.transpose(0, 1), v, "teacher_index"), (i[:1], v, "teacher_index"),
+                              (i.reshape(4, 9), v, "teacher_index"), (i, v.transpose(0, 1), "teacher_logits"),
+                              (i, v.reshape(2, 9, 2), "teacher_logits"), (i, v[..., :2], "teacher_logits"),
+                              (i, v.reshape(4, 9), "teacher_logits")):
+        with pytest.raises(ValueError, match=name):
+            GF.topk_distillation(x, ids, values)
+    X, W = torch.zeros(12, 8), torch.zeros(9, 8)
+    for ids, values, name in ((i[0], v[0], "teacher_index"), (i.reshape(12, 3), v[0], "teacher_logits"),
+                              (i, v, "teacher_index"), (i.reshape(12, 3), v.reshape(3, 12).t()[:, :2], "teacher_logits")):
+        with pytest.raises(ValueError, match=name):
+            GF.chunked_linear_topk_distillation(X, W, ids, values)
