@@ -162,7 +162,7 @@ def selective_log_softmax(logits, index):
 def _dense_rows(logits):
     """[..., V] logits as [rows, V] with dense rows (a copy only where the layout needs one)."""
     x = logits if logits.dim() == 2 else logits.reshape(-1, logits.shape[-1])
-    if x.shape[1] > 1 and (x.stride(1) != 1 or (x.shape[0] > 1 and x.stride(0) < x.shape[1])):
+    if (x.shape[1] > 1 and x.stride(1) != 1) or (x.shape[0] > 1 and x.stride(0) < x.shape[1]):
         x = x.contiguous()
     return x
 

@@ -164,3 +164,13 @@ def test_functional_forms_refuse_companions_of_another_shape():
                               (i, v, "teacher_index"), (i.reshape(12, 3), v.reshape(3, 12).t()[:, :2], "teacher_logits")):
         with pytest.raises(ValueError, match=name):
             GF.chunked_linear_topk_distillation(X, W, ids, values)
+
+
+def test_dense_rows_of_a_vocabulary_of_one():
+    """Rows that share their one logit (a broadcast) are copied like any others that overlap."""
+    from lm_head_cross_gh_b200 import functional as GF
+    for V in (1, 3):
+        x = GF._dense_rows(torch.ones(1, V).expand(4, V))
+        assert x.shape == (4, V) and x.stride(0) >= V and (V == 1 or x.stride(1) == 1)
+    x = torch.ones(4, 6)[:, :1]
+    assert GF._dense_rows(x) is x
