@@ -564,8 +564,11 @@ def _row_output(t, name: str, dtype, shape, device, torch, like=None):
 
 
 def _grad_like(grad, logits, B, V, ld, torch):
-    """The gradient's tensor and row stride (by default laid out as the logits)."""
+    """The gradient's tensor and row stride: by default the logits', or for rows far
+    apart (one position's out of [B, S, V]) the least with the same offsets from 16 bytes."""
     if grad is None:
+        if ld > 2 * V:
+            ld = V + (ld - V) % (16 // logits.element_size())
         return torch.empty_strided((B, V), (ld, 1), dtype=logits.dtype, device=logits.device), ld
     if grad is logits:
         return grad, ld
@@ -632,7 +635,8 @@ def gh_token_logprobs_vjp(logits, index, lse, entropy, g_logprob, g_entropy=None
     ``gh_token_logprobs``, ``lse`` and ``entropy`` as it returned; ``g_logprob``
     and ``g_entropy`` (None for none) the upstream gradients, float32 [B].
     ``grad`` (optional output, may be ``logits`` itself) is allocated with the
-    logits' row stride when not given.  Returns ``grad``.
+    logits' row stride when not given (with a smaller one where the logits' rows
+    are more than 2 V apart).  Returns ``grad``.
     """
     import torch
     B, V, ld, dtype = _rows(logits, torch)

@@ -622,3 +622,22 @@ def test_functional_companions_may_be_flat(cuda_device):
     l1 = GF.topk_distillation(x, ids, top, 2.0)
     l2 = GF.topk_distillation(x, ids.reshape(12, 5), top.reshape(12, 5), 2.0)
     assert torch.equal(l1, l2)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_rows_far_apart(cuda_device, dtype):
+    """One position's logits out of [B, S, V]: values, gradients, and memory of their own size."""
+    B, S, V, k = 40, 33, 2003, 6
+    whole = logits(B * S, V, dtype, 7).view(B, S, V)
+    t = given(B, V, 7)
+    x = whole[:, -1]
+    out = gh.gh_token_logprobs(x, t, k)
+    check_logprobs(x, t, k, 1.0, out)
+    gl, gH = torch.randn(B, device="cuda"), torch.randn(B, device="cuda")
+    grad = gh.gh_token_logprobs_vjp(x, t, out[2], out[1], gl, gH)
+    assert grad.stride(0) < V + 8
+    check_vjp(x, t, gl, gH, 1.0, grad)
+    leaf = whole.clone().requires_grad_(True)
+    lp, ent = GF.token_logprobs(leaf[:, -1], t)
+    (gl * lp + gH * ent).sum().backward()
+    assert torch.equal(leaf.grad[:, -1], grad) and not leaf.grad[:, :-1].any()

@@ -174,3 +174,16 @@ def test_dense_rows_of_a_vocabulary_of_one():
         assert x.shape == (4, V) and x.stride(0) >= V and (V == 1 or x.stride(1) == 1)
     x = torch.ones(4, 6)[:, :1]
     assert GF._dense_rows(x) is x
+
+
+@pytest.mark.parametrize("dtype,step", [(torch.float32, 4), (torch.bfloat16, 8)])
+def test_the_gradient_of_rows_far_apart_is_not_as_wide(dtype, step):
+    """The gradient's own rows (one position's logits out of [B, S, V]): close
+    together, each at its logits' offset from 16 bytes; a padded head's keep their stride."""
+    for S, V in ((64, 101), (3, 64), (1000, 7), (5, 1)):
+        x = torch.zeros(6, S, V, dtype=dtype)[:, -1]
+        grad, ld = gh._grad_like(None, x, 6, V, S * V, torch)
+        assert grad.shape == (6, V) and grad.stride(0) == ld and V <= ld < V + step and (ld - S * V) % step == 0
+        assert grad.untyped_storage().nbytes() <= 6 * (V + step) * grad.element_size()
+    x = torch.zeros(6, 104, dtype=dtype)[:, :101]
+    assert gh._grad_like(None, x, 6, 101, 104, torch)[1] == 104
