@@ -340,7 +340,8 @@ gh_status_t gh_token_logprobs_vjp(const void* logits, int64_t ld, const int64_t*
  *     scale    = 1 / max(n, 1) for GH_REDUCTION_MEAN, 1 for SUM
  *     loss     = scale * sum of row losses
  * where n counts the rows with an entry.  Rows without one have no loss and a
- * zero gradient, and their logits are not read.
+ * zero gradient, whatever their logits hold (any memory of the batch may be
+ * read, theirs too).
  *
  *   logits   [B, V] of `dtype`, device, rows `ld` elements apart (ld >= V).
  *   teacher_index  [B, K] int64, teacher_logits [B, K] float32, device; an id

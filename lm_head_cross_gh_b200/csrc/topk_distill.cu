@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(32 * (W + 1), 27 / (W + 1)) distill_kernel(Dis
   uint4 qa[kBatch], qb[kBatch];
   const int first = warp < W ? warp * kBatchChunks : nc;
   int c0 = first;
-  load(qa, c0);  // (before it is known whether the row counts)
+  load(qa, c0);  // before it is known whether the row counts (after it: 0.5 to 2% slower)
   if (!a.flags) mark_rows(a, sh.has, kThreads);
   const bool counts = (a.flags ? a.flags[row] : sh.has[row]) != 0;
   constexpr int kEnds = W;  // the warp of the teacher's side
