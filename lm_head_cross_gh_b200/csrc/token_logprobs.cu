@@ -39,28 +39,27 @@ namespace {
 // distributed shared memory.
 //
 // Bound by HBM where no alternatives are asked for: [4096, 50257] fp32 in 120
-// us (6.8 TB/s), [8192, 50257] bf16 in 128 us from a cool start (6.4 TB/s) and
-// 133 to 147 under the power cap, with the special-function unit 67% busy.  The
-// segments' maxima (41 warp instructions more a batch of 2 KiB a warp, on 176)
-// and the row's end (2,500 with 20 alternatives) bound it with alternatives, by
-// their instructions: [4096, 50257] bf16 with 32 in 91 to 96 us, [1024, 262144]
-// with 128 in 110 to 118, [4096, 50257] fp32 with 32 in 147 to 153.
+// us (6.8 TB/s), [8192, 50257] bf16 in 125 us from a cool start (6.5 TB/s) and
+// 131 to 148 under the power cap, with the special-function unit 67% busy.  With
+// alternatives the segments' maxima (41 warp instructions more a batch of 2 KiB a
+// warp, on 176) and the row's end (2,500 with 20 alternatives) add instructions,
+// and at the end one warp picks segments while others wait (barrier stalls 1.1 per
+// issue; no unit is full, issue slots 55%): [4096, 50257] bf16 with 32 in 90 to 96
+// us, [1024, 262144] with 128 in 107 to 120, [4096, 50257] fp32 with 32 in 147 to 155.
 //
-// Beside an earlier form of this one that took 150 us at [8192, 50257] bf16: a
-// ring of bulk copies with consumer and finalizer warps 162 us (its row ends
-// keep one warp busy for longer than a row lasts: 328 us with 20 alternatives,
-// 196 there, 163 to 174 now), two warps per CTA 152, eight 166, CTAs that take over the
-// next row through launch control 172 (it spills).  A ring of asynchronous
-// copies per warp 146 to 149 (137 then without it); a CTA more per SM with
-// alternatives (64 registers for 72) 93.5 for 91.3 at [4096, 50257] with 32,
-// 126 for 110 at [1024, 262144] with 128.
+// Warps per CTA, on one board in turn, at [8192, 50257] bf16 / [1024, 262144] bf16
+// / [4096, 50257] fp32 without alternatives, and with 32 / 128 / 32: 4 139 / 110 /
+// 123 and 189 / 120 / 158 us, 2 141 / 124 / 123 and 180 / 216 / 199, 8 150 / 93 / 123 and
+// 242 / 126 / 183; 4 and a CTA more per SM with alternatives (64 registers for 72)
+// 193 / 143 / 162.  At 72 registers the fp32 kernels with alternatives and the bf16
+// one of split rows with finer segments spill 4 to 40 bytes a thread.
 // ---------------------------------------------------------------------------
 
 constexpr int kLpWarps = 4;
 // Rows of up to 16 KiB take CTAs of one warp once there are more of them than
 // CTAs of four are resident: the fixed work of a row's end is then one warp's
-// ([4750, 1204] bf16 with 2 alternatives 23.8 -> 14.5 us, [4000, 8192] with 20
-// 33.3 -> 27.6; 32 KiB rows lose: [2000, 16384] 21.2 -> 27.9).
+// ([4750, 1204] bf16 with 2 alternatives 23.7 -> 14.0 us, [4000, 8192] with 20
+// 30.5 -> 25.9; 32 KiB rows lose: [2000, 16384] 21.1 -> 28.8).
 constexpr int64_t kShortChunks = 1024;
 constexpr int kMaxSlices = 8;       // CTAs per row: a portable cluster
 constexpr int kLpMaxSegs = 16384;   // 512-byte segments of a CTA whose keys are kept (64 KiB)
@@ -79,9 +78,9 @@ enum SegKind : int { kSegElement = 0, kSegChunk = 1, kSegQuad = 2, kSegWarp = 3 
 enum TopMode : int { kTopNone = 0, kTopWarp = 1, kTopFine = 2 };
 
 // How many segments may be listed for k alternatives.  A few more than k end the
-// search for a threshold sooner: [1, 50257] bf16 with 20 alternatives 10.5 -> 9.2
-// us, [214, 22627] fp32 with 36 17.4 -> 15.2; k / 4 + 4 more gain the same there,
-// but cost more ranking: [2701, 3400] fp32 with 107 31.1 -> 32.6 us.
+// search for a threshold sooner: [1, 50257] bf16 with 20 alternatives 10.9 -> 9.9
+// us, [214, 22627] fp32 with 36 17.8 -> 16.1, [2701, 3400] fp32 with 107 32.6 ->
+// 31.4; many more would cost more ranking.
 __host__ __device__ constexpr int most_listed(int k) { return k + k / 8 + 2; }
 
 template <int W>
@@ -549,7 +548,7 @@ __global__ void __launch_bounds__(32 * W, kLpResident<TOP, W>) logprobs_kernel(L
       if constexpr (TOP != kTopNone) {
         // The parts' alternatives in the row's order, then as logits of a row whose
         // segments are single logits; up to 64 are all ranked ([142, 167081] bf16
-        // with 4 alternatives 22.4 -> 21.0 us; 96 of them lose, 10.5 -> 10.7).
+        // with 4 alternatives 23.6 -> 22.0 us; at 80, [1, 50257] with 10, both take 9.1).
         const int total = a.slices * a.top_k;
         const bool pick = total > 64;
         uint64_t* const gathered = reinterpret_cast<uint64_t*>(seg_keys + (total + 127) / 128 * 128);
@@ -602,15 +601,18 @@ __global__ void __launch_bounds__(32 * W, kLpResident<TOP, W>) logprobs_kernel(L
 //
 // One CTA of four warps per part of a row (parts of about 32 KiB), eight on an
 // SM; the warps stream batches as the forward does.  Bound by HBM: [8192, 50257]
-// bf16 in 247 to 257 us and [1024, 128256] fp32 in 158, both at the copy rate.  The
-// parts' size matters because the CTAs in flight then read and write one stretch
-// of memory: 16 KiB 258 / 155 us, 64 KiB 259 / 164, 128 KiB 269 / 167, and whole
-// rows as tiles of one persistent grid 303 / 167.
+// bf16 in 246 to 268 us and [1024, 128256] fp32 in 158 to 170, both at the copy rate
+// (the bf16 kernel spills 28 bytes a thread at 64 registers).  The parts' size
+// matters because the CTAs in flight then read and write one stretch of memory:
+// [8192, 50257] bf16 / [4096, 50257] fp32 249 / 246 us, with parts of 16 KiB 256 / 243,
+// of 64 KiB 259 / 253.
 // ---------------------------------------------------------------------------
 
 // Beyond this |lse| its fp32 rounding (2^-14 here) would show in exp(x / T -
-// lse): rows whose logits all lie far from 0, such as fully masked ones, have
-// their max and sum taken again.
+// lse): rows whose logits all lie far from 0, such as fully masked ones, and
+// ordinary ones at low temperatures (logits near 10 from T = 0.01 down) have their
+// max and sum taken again, by the CTA of their first part alone: [8192, 50257] bf16
+// 704 us where every row is one, 249 otherwise.
 constexpr float kFarLse = 1024.0f;
 
 constexpr int kLpVjpWarps = 4;

@@ -19,21 +19,19 @@
 // differ.  HBM sees one read and one write of every logit (240 MB read for 238
 // MB of logits at [2368, 50257] bf16).
 //
-// [8192, 50257] bf16 with 32 entries: 316 to 335 us, [1024, 262144] bf16 with
-// 128: 214 to 222, [4096, 50257] fp32 with 32: 312 to 326 (boards and clocks
-// differ): 4.4 to 5 TB/s of HBM traffic with the special-function unit 62%
-// (fp32 32%) and the issue slots 46% (30%) busy; the second reading of every row
-// through L2 and the wait between the passes are what a gradient from known sums
-// (247 us for the bf16 case) does not have.  Warps x CTAs per SM on the bf16 and fp32
-// cases, before the last changes: 7 x 3 343 / 317, 7 x 4 371 / 327, 9 x 3 356 /
-// 320, 15 x 2 356 / 356, 11 x 2 352 / 342, 5 x 5 393 / 371; 7 to 10 x 3 are now
-// alike.  Rows are split over a cluster from 128 KiB on: at 256 KiB the rows in
-// flight outgrow L2 (fp32 382 us, [1024, 262144] 270 against 241), at 64 KiB the
-// exchanges cost more (424 us for the bf16 rows).  Also tried: sums and
-// gradients as items of 32 KiB handed out in an order that keeps a row in L2
-// (462 / 403 us, the items' ends), a quarter of the exponentials as polynomials
-// (355 us and more), each CTA finding out itself whether its row has an entry (326
-// us for 318).
+// [8192, 50257] bf16 with 32 entries: 310 to 338 us, [1024, 262144] bf16 with
+// 128: 213 to 226, [4096, 50257] fp32 with 32: 313 to 326 (boards and clocks
+// differ), the loss alone 161, 114 and 163.  4.4 TB/s of HBM traffic at [2368,
+// 50257] bf16 with the special-function unit 62% and the issue slots 46% busy: no
+// unit is full; the streaming warps wait for the row's sum between the passes
+// (barrier stalls 2.4 per issue), and three CTAs on an SM do not fill that.
+//
+// Warps x CTAs per SM, on one board in turn, at those three shapes: 8 x 3 325 /
+// 219 / 325 us, 4 x 5 351 / 242 / 356, 6 x 4 312 / 234 / 322, 7 x 3 332 / 227 / 325,
+// 9 x 3 340 / 229 / 322, 12 x 2 355 / 254 / 372 (6 x 4 would need a rule on the row's
+// length).  Rows are split over a cluster from 128 KiB on: at 256 KiB the rows in
+// flight outgrow L2 (324 / 236 / 344), at 64 KiB the exchanges cost more (430 / 293 /
+// 432).
 #include "ce.h"
 #include "linear_ce.h"
 #include "profile.h"
@@ -46,13 +44,13 @@ namespace {
 
 // Warps that stream a row (one more has the teacher's side); and for rows of up
 // to 32 KiB, once there are more of them than the larger CTAs are resident
-// ([3383, 5056] bf16 with 54 entries 63 -> 34 us, [4000, 16384] with 16 78 -> 70;
-// 64 KiB rows lose: [4000, 32768] 115 -> 140).
+// ([3383, 5056] bf16 with 54 entries 55 -> 30 us, [4000, 16384] with 16 73 -> 66;
+// 64 KiB rows lose: [4000, 32768] 108 -> 132).
 constexpr int kDistillWarps = 8, kDistillShortWarps = 2;
 constexpr int64_t kDistillShortChunks = 2048;
 constexpr int kLaneEntries = GH_MAX_TOP_K / 32;
 // CTAs of the counting kernel, its latency being a few rows' a warp ([8192, 50257]
-// 334 us a call with 64, 330 with 256; [1766, 1252] 19.3, 18.9).
+// 332 us with 64, 323 with 256; [3383, 5056] 33.3, 30.4; [1766, 1252] 18.1, 18.4).
 constexpr int kCountParts = 256;
 
 __device__ __forceinline__ bool distill_entry(int64_t id, float v, int64_t V) {
@@ -94,7 +92,11 @@ __global__ void __launch_bounds__(256) distill_count_kernel(const int64_t* __res
 }
 
 // Batches of up to this many rows and entries are counted by every CTA itself
-// instead of by a kernel before it: a launch less, 3 us of a call's 18 at [64, 1024].
+// instead of by a kernel before it.  A call is the faster for that up to about 1024
+// entries (11.2 us for 13.5 at [64, 1024] with 8 and [32, 1024] with 32; at 2048
+// entries 11.5 for 13.5 with V = 1024, 15.0 for 13.5 with 50257); in a replayed
+// graph, where a launch costs less, up to about 512 (8.0 for 9.3 us at 256, 8.7 for
+// 9.3 at 512, 9.5 for 9.3 at 1024, 11.2 for 9.4 at 2048).
 constexpr int kCountInside = 64;
 constexpr int64_t kCountInsideEntries = 2048;
 
@@ -431,9 +433,9 @@ __global__ void __launch_bounds__(32 * (W + 1), 27 / (W + 1)) distill_kernel(Dis
   }
   if (!with_grad) return;
   if (e >= 0) Elem<T>::store(dst + e * ES, coef * ex2(fmaf(edge - d.sub, a.c, -d.r)));
-  // Full batches of ordinary rows know their alignment beforehand: 343 -> 332 us
-  // at 8192 x 50257; two warps per CTA gain nothing by it (33.8 -> 35.2 us at
-  // 3383 x 5056) and test it per chunk.
+  // Full batches of ordinary rows know their alignment beforehand: 342 -> 323 us
+  // at 8192 x 50257.  Two warps per CTA test it per chunk (30.4 us for 30.0 at
+  // 3383 x 5056, 66.0 for 62.6 at 4000 x 16384).
   constexpr bool kKnown = W > kDistillShortWarps;
   const bool plain = d.sub == 0.0f && (!kKnown || congruent);
   auto put = [&](const uint4 (&q)[kBatch], int at) {
