@@ -19,6 +19,7 @@
  *  - gh_token_logprobs, gh_token_logprobs_vjp, gh_topk_distill: log-probabilities
  *    with entropy and alternatives, their gradient, and distillation from a
  *    teacher's top logits; the Greyhound API has no counterpart.
+ *  - gh_scale_grad: a stored gradient times the scalar upstream gradient.
  *  - gh_linear_ce: `chunked_linear_cross_entropy` — logits = inputs @ weight.T
  *    computed one row chunk at a time and never materialised in full; per
  *    chunk the logits gradient G gives grad_inputs[chunk] = G @ weight and
